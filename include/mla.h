@@ -252,6 +252,43 @@ mla_status mla_cache_truncate_paged(uint16_t *pool, const int32_t *page_table, i
                                     void *stream);
 
 /*
+ * The latent cache in 4 bits ("packed"): a row of R = 512 latents takes 288 bytes,
+ *   bytes 0..255    e2m1 codes, latent 2k in the low nibble of byte k, 2k + 1 in the high one
+ *   bytes 256..287  e4m3 scales, byte 256 + g for latents 16 g .. 16 g + 15
+ *   c[i] = unit * scale[i / 16] * code[i],  code in +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}
+ * with unit a power of two in [2^-64, 2^64] that the caller chooses once for a cache: scales hold
+ * 2^-9 .. 448 (full precision from 2^-6), so unit should bring the rows' largest values to the
+ * order of 1 to 1000.  Pages are those of the bf16 pool: pool [num_pages, 64, 288] uint8, position j
+ * of sequence b is pool[page_table[b, j / 64], j % 64].  The pages describe no 4-bit cache.
+ *
+ * mla_cache_append_packed: mla_cache_append_paged with quantisation.  For each group of 16 latents
+ *   y = x / unit, scale = e4m3(max|y| / 6) and code = e2m1(y / scale), both to nearest with ties to
+ *   even, at most 448 and 6; a scale of zero gives codes of zero; a group that holds an Inf or a NaN
+ *   gets the scale NaN.  rows [B, Q, R] bf16, seq_lens in/out; Q <= 4,194,240.
+ * mla_cache_truncate_packed: as mla_cache_truncate_paged; the discarded rows become zero bytes.
+ * mla_cache_unpack: rows[b, i] = the bf16 values at position start[b] + i, i < n (exact: a value has
+ *   six significant bits), for example for mla_expand_kv.  rows [B, n, R] bf16, start [B] int32.  A
+ *   position outside the table or on an unmapped page gives a zero row and MLA_ERR_INDEX.
+ * mla_attend_packed: attention over the packed rows; window and sinks as for mla_attend_window_*,
+ *   window = 0 sees every row up to the query's own.  q_tilde, outputs, workspace as for
+ *   mla_attend_paged; max_pages * 64 < 2^31 - 128.  Pages without a visible row need not be mapped.
+ *   An Inf or NaN in rows that no query sees has no effect; a NaN in a seen row gives NaN.
+ */
+mla_status mla_cache_append_packed(uint8_t *pool, const int32_t *page_table, int32_t *seq_lens, const uint16_t *rows,
+                                   int B, int Q, int R, int page_size, int max_pages, int num_pages, float unit,
+                                   int32_t *status, void *stream);
+mla_status mla_cache_truncate_packed(uint8_t *pool, const int32_t *page_table, int32_t *seq_lens, const int32_t *keep,
+                                     int B, int Q, int R, int page_size, int max_pages, int num_pages,
+                                     int32_t *status, void *stream);
+mla_status mla_cache_unpack(const uint8_t *pool, const int32_t *page_table, const int32_t *start, uint16_t *rows, int B,
+                            int n, int R, int page_size, int max_pages, int num_pages, float unit, int32_t *status,
+                            void *stream);
+mla_status mla_attend_packed(const uint16_t *q_tilde, const uint8_t *pool, const int32_t *page_table,
+                             const int32_t *seq_lens, int B, int Q, int H, int R, int page_size, int max_pages,
+                             int num_pages, float unit, int window, int sinks, float scale, void *workspace,
+                             size_t ws_bytes, uint16_t *o_latent, float *lse, int32_t *status, void *stream);
+
+/*
  * k-pool index producer for mla_attend_indexed.  Page "GLM-5.3-Flash engine (c/glm53.c)"
  * (colibri docs), Architecture notes, DSA with k-pooling: keys are grouped into pools of
  * `pool` consecutive positions, a pool's key is a per-channel softmax mixture of its

@@ -17,13 +17,15 @@ LIB_PATH = os.path.join(_HERE, "libmla_b200.so")
 MLA_OK, MLA_ERR_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA, MLA_ERR_WORKSPACE, MLA_ERR_INDEX, MLA_ERR_TIMEOUT = range(7)
 MODE_DENSE, MODE_PAGED, MODE_INDEXED = 0, 1, 2
 H, D, R, PAGE = 64, 256, 512, 64
+PACKED_ROW = R // 2 + R // 16  # bytes of a row of the 4-bit cache
 SCALE = 1.0 / 16.0
 
 EXPORTS = ("mla_status_string", "mla_last_error_string", "mla_absorb_q", "mla_attend_dense", "mla_attend_paged", "mla_attend_indexed",
            "mla_up_proj", "mla_attend_workspace_bytes", "mla_debug_gather", "mla_attend_dense_noalloc",
            "mla_cache_append_dense", "mla_cache_append_paged", "mla_cache_truncate_dense", "mla_cache_truncate_paged",
            "mla_debug_wait_timeout", "mla_kpool_keys", "mla_kpool_select", "mla_attend_up_dense",
-           "mla_attend_up_paged", "mla_attend_up_indexed", "mla_expand_kv", "mla_prefill_expanded")
+           "mla_attend_up_paged", "mla_attend_up_indexed", "mla_expand_kv", "mla_prefill_expanded",
+           "mla_cache_append_packed", "mla_cache_truncate_packed", "mla_cache_unpack", "mla_attend_packed")
 
 
 class MLAError(RuntimeError):
@@ -75,6 +77,13 @@ def lib():
     L.mla_prefill_expanded.argtypes = [vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp, vp]
     L.mla_debug_wait_timeout.argtypes = [ctypes.c_longlong, vp, vp]
     L.mla_debug_wait_timeout.restype = ctypes.c_int32
+    L.mla_cache_append_packed.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, vp]
+    L.mla_cache_truncate_packed.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp]
+    L.mla_cache_unpack.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, vp]
+    L.mla_attend_packed.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, f32, i32, i32, f32, vp, sz, vp,
+                                    vp, vp, vp]
+    for name in ("mla_cache_append_packed", "mla_cache_truncate_packed", "mla_cache_unpack", "mla_attend_packed"):
+        getattr(L, name).restype = ctypes.c_int32
     for name in ("mla_absorb_q", "mla_up_proj", "mla_attend_dense", "mla_attend_paged", "mla_attend_indexed",
                  "mla_debug_gather", "mla_attend_dense_noalloc", "mla_cache_append_dense", "mla_cache_append_paged",
                  "mla_cache_truncate_dense", "mla_cache_truncate_paged", "mla_attend_up_dense", "mla_attend_up_paged",
@@ -460,6 +469,71 @@ def mla_cache_truncate_paged(pool, page_table, seq_lens, keep, q_len, status=Non
     _check("mla_cache_truncate_paged", lib().mla_cache_truncate_paged(
         _ptr(pool), _ptr(page_table), _ptr(seq_lens), _ptr(keep), seq_lens.shape[0], q_len, R, pool.shape[1],
         page_table.shape[1], pool.shape[0], _ptr(status), _stream(stream)))
+
+
+def _check_packed(pool, page_table, B, what, status):
+    _require(pool, "pool", "u8", (None, PAGE, PACKED_ROW))
+    _require(page_table, "page_table", "i32", (None, None))
+    if page_table.shape[0] < B:
+        raise ValueError(f"page_table has {page_table.shape[0]} rows, {what} {B} sequences")
+    _require(status, "status", "i32", min_numel=1, optional=True)
+
+
+def mla_cache_append_packed(pool, page_table, seq_lens, rows, unit=1.0, status=None, stream=None):
+    """Append rows [B, Q, R] bf16, quantised to 4 bits, through page_table [B, max_pages] into
+    pool [P, 64, 288] uint8; seq_lens [B] int32 advances by Q (in place)."""
+    _require(rows, "rows", "bf16", (None, None, R))
+    B, Q = rows.shape[0], rows.shape[1]
+    _check_packed(pool, page_table, B, "rows", status)
+    _require(seq_lens, "seq_lens", "i32", min_numel=B)
+    _check_cuda(pool, page_table, seq_lens, rows, status)
+    _check("mla_cache_append_packed", lib().mla_cache_append_packed(
+        _ptr(pool), _ptr(page_table), _ptr(seq_lens), _ptr(rows), B, Q, R, PAGE, page_table.shape[1], pool.shape[0],
+        unit, _ptr(status), _stream(stream)))
+
+
+def mla_cache_truncate_packed(pool, page_table, seq_lens, keep, q_len, status=None, stream=None):
+    """Keep the first keep[b] of the last q_len rows of each sequence of a 4-bit pool; zero the rest."""
+    _require(seq_lens, "seq_lens", "i32", (None,))
+    B = seq_lens.shape[0]
+    _require(keep, "keep", "i32", min_numel=B)
+    _check_packed(pool, page_table, B, "seq_lens", status)
+    _check_cuda(pool, page_table, seq_lens, keep, status)
+    _check("mla_cache_truncate_packed", lib().mla_cache_truncate_packed(
+        _ptr(pool), _ptr(page_table), _ptr(seq_lens), _ptr(keep), B, q_len, R, PAGE, page_table.shape[1],
+        pool.shape[0], _ptr(status), _stream(stream)))
+
+
+def mla_cache_unpack(pool, page_table, start, n, unit=1.0, rows=None, status=None, stream=None):
+    """The values of positions start[b] .. start[b] + n - 1 of a 4-bit pool: rows [B, n, R] bf16."""
+    import torch
+    _require(start, "start", "i32", (None,))
+    B = start.shape[0]
+    _check_packed(pool, page_table, B, "start", status)
+    _require(rows, "rows", "bf16", (B, n, R), optional=True)
+    _check_cuda(pool, page_table, start, rows, status)
+    if rows is None:
+        rows = torch.empty(B, n, R, dtype=torch.bfloat16, device=pool.device)
+    _check("mla_cache_unpack", lib().mla_cache_unpack(
+        _ptr(pool), _ptr(page_table), _ptr(start), _ptr(rows), B, n, R, PAGE, page_table.shape[1], pool.shape[0],
+        unit, _ptr(status), _stream(stream)))
+    return rows
+
+
+def mla_attend_packed(q_tilde, pool, page_table, seq_lens, unit=1.0, window=0, sinks=0, scale=SCALE, workspace=None,
+                      o_latent=None, lse=None, status=None, want_lse=True, stream=None):
+    """Attention over a 4-bit pool [P, 64, 288] uint8; with window > 0 each query sees its last
+    `window` rows and the first `sinks` ones."""
+    B, Q = _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens, seq_lens_required=True)
+    _check_packed(pool, page_table, B, "q_tilde", status)
+    _check_cuda(q_tilde, pool, page_table, seq_lens, workspace, o_latent, lse, status)
+    workspace = new_workspace(B, Q) if workspace is None else workspace
+    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
+    _check("mla_attend_packed", lib().mla_attend_packed(
+        _ptr(q_tilde), _ptr(pool), _ptr(page_table), _ptr(seq_lens), B, Q, H, R, PAGE, page_table.shape[1],
+        pool.shape[0], unit, window, sinks, scale, _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(o_latent), _ptr(lse), _ptr(status), _stream(stream)))
+    return o_latent, lse
 
 
 def mla_debug_wait_timeout(limit_cycles, status, stream=None):

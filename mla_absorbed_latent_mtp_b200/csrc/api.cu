@@ -8,6 +8,8 @@
 
 #include "mla.h"
 #include "internal.h"
+#include "packed.cuh"
+#include "packed_attend.h"
 
 namespace mla {
 
@@ -43,6 +45,17 @@ bool make_map(CUtensorMap *map, const void *ptr, int rank, const uint64_t *dims,
                   estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+// The same for bytes, with or without the 128-byte swizzle.
+bool make_bytes_map(CUtensorMap *map, const void *ptr, int rank, const uint64_t *dims, const uint64_t *strides,
+                    const uint32_t *box, bool swizzle) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint32_t estride[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void *>(ptr), dims, strides, box, estride,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -186,6 +199,65 @@ static mla_status attend_common(int mode, const uint16_t *q_tilde, const uint16_
   return cuda_status(launch_merge_up(tm_w, p, mode, out, st));
 }
 
+static mla_status attend_packed_common(const uint16_t *q_tilde, const uint8_t *pool, const int32_t *page_table,
+                                       const int32_t *seq_lens, int B, int Q, int H, int R, int page_size,
+                                       int max_pages, int num_pages, float unit, int window, int sinks, float scale,
+                                       void *workspace, size_t ws_bytes, uint16_t *o_latent, float *lse,
+                                       int32_t *status, void *stream) {
+  if (q_tilde == nullptr || pool == nullptr || page_table == nullptr || seq_lens == nullptr || o_latent == nullptr)
+    return MLA_ERR_ARG;
+  if (B < 1 || Q < 1 || !isfinite(scale) || !packed::valid_unit(unit)) return MLA_ERR_ARG;
+  if (window < 0 || sinks < 0 || max_pages < 1 || num_pages < 1) return MLA_ERR_ARG;
+  if (H != kHeads || R != kLatent || page_size != kPageTokens) return MLA_ERR_UNSUPPORTED;
+  if (!aligned16(q_tilde) || !aligned16(pool) || !aligned16(o_latent)) return MLA_ERR_UNSUPPORTED;
+  if ((long long)B * Q * H >= (1LL << 31)) return MLA_ERR_ARG;
+  if ((long long)num_pages * kPageTokens >= (1LL << 31)) return MLA_ERR_ARG;
+  if ((long long)max_pages * kPageTokens >= (1LL << 31) - 128) return MLA_ERR_ARG;  // positions and tile ends are int32
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return cuda_status(e);
+  const int sms = sm_count_for(dev);
+  if (workspace == nullptr || ws_bytes < attend_workspace_bytes_for(B, Q, sms) || !aligned16(workspace))
+    return MLA_ERR_WORKSPACE;
+  CUtensorMap tm_codes, tm_scales;
+  {
+    // a row's 256 code bytes as two halves of 128: one box {128 bytes, 64 rows, 2} is a page's codes
+    const uint64_t rows = (uint64_t)num_pages * kPageTokens;
+    const uint64_t dims[3] = {128, rows, 2};
+    const uint64_t strides[2] = {packed::kRowBytes, 128};
+    const uint32_t box[3] = {128, kPageTokens, 2};
+    if (!make_bytes_map(&tm_codes, pool, 3, dims, strides, box, true)) return cuda_status(cudaErrorInvalidValue);
+    const uint64_t sdims[2] = {packed::kScaleBytes, rows};
+    const uint32_t sbox[2] = {packed::kScaleBytes, kPageTokens};
+    if (!make_bytes_map(&tm_scales, pool + packed::kCodeBytes, 2, sdims, strides, sbox, false))
+      return cuda_status(cudaErrorInvalidValue);
+  }
+  AttendPackedParams p = {};
+  p.a.seq_lens = seq_lens;
+  p.a.page_table = page_table;
+  p.a.B = B;
+  p.a.Q = Q;
+  p.a.Lmax = max_pages * kPageTokens;
+  p.a.max_pages = max_pages;
+  p.a.num_pages = num_pages;
+  p.a.group_size = Q;
+  p.a.groups = std::max(1, sms / Q);
+  const size_t slots = attend_slots(B, Q, sms);
+  p.a.part_o = reinterpret_cast<float *>(workspace);
+  p.a.part_m = p.a.part_o + slots * kHeads * kLatent;
+  p.a.part_l = p.a.part_m + slots * kHeads;
+  p.a.seq_ts = reinterpret_cast<long long *>(p.a.part_l + slots * kHeads);
+  p.a.seq_nt = reinterpret_cast<int32_t *>(p.a.seq_ts + (size_t)B * Q);
+  p.a.o_latent = o_latent;
+  p.a.lse = lse;
+  p.a.status = status;
+  p.q_tilde = q_tilde;
+  p.window = window;
+  p.sinks = sinks;
+  p.unit = unit;
+  p.score_factor = scale * 1.4426950408889634f * unit;
+  return cuda_status(launch_attend_packed(tm_codes, tm_scales, p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 static mla_status proj_common(bool absorb, const uint16_t *x, const uint16_t *w, uint16_t *out, int n, int H, int D,
                               int R, void *stream) {
   if (x == nullptr || w == nullptr || out == nullptr) return MLA_ERR_ARG;
@@ -303,6 +375,14 @@ const char *mla_status_string(mla_status s) {
 mla_status mla_absorb_q(const uint16_t *q, const uint16_t *w_uk, uint16_t *q_tilde, int n, int H, int D, int R,
                         void *stream) {
   return mla::proj_common(true, q, w_uk, q_tilde, n, H, D, R, stream);
+}
+
+mla_status mla_attend_packed(const uint16_t *q_tilde, const uint8_t *pool, const int32_t *page_table,
+                             const int32_t *seq_lens, int B, int Q, int H, int R, int page_size, int max_pages,
+                             int num_pages, float unit, int window, int sinks, float scale, void *workspace,
+                             size_t ws_bytes, uint16_t *o_latent, float *lse, int32_t *status, void *stream) {
+  return mla::attend_packed_common(q_tilde, pool, page_table, seq_lens, B, Q, H, R, page_size, max_pages, num_pages,
+                                   unit, window, sinks, scale, workspace, ws_bytes, o_latent, lse, status, stream);
 }
 
 mla_status mla_up_proj(const uint16_t *o_latent, const uint16_t *w_uv, uint16_t *out, int n, int H, int D, int R,

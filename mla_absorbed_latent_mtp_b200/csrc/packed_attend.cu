@@ -1,0 +1,879 @@
+// packed_attend.cu -- split-L latent attention over the 4-bit paged cache (packed.cuh):
+//   s_j = scale q~ . c_j,  a = softmax over the rows a query sees (window.cuh),  o = sum_j a_j c_j.
+//
+// Work decomposition: as attend.cu (a list of the tiles of all sequences, split into equal
+// ranges over CTA groups of one CTA per query of a verify window; partials in the workspace;
+// a combine kernel), with tiles of 128 rows, two pages.
+//
+// What bounds it.  A tile is 36 KB of cache but 16.8 MFLOP per query, 2,048 cycles of the
+// tensor core at N = 64: bytes cost at most half of that, so the kernel has to keep the MMAs
+// fed.  An MMA that reads both operands from shared memory takes 48.5 cycles (M = 128, N = 64,
+// measured back to back), with its A operand in tensor memory 32.4, the full rate; and 4-bit
+// codes cannot be an operand as they are, since each row has its own scales.  So the cache
+// operand is unpacked into TENSOR memory, twice, by register, and shared memory holds only the
+// packed rows, q~ and P:
+//   S^T[rows, heads]    = C (A: 128 rows on the lanes, 64 latents a chunk) * Q~^T (smem)
+//   O^T[latent, heads] += C^T (A: 128 latents on the lanes, 16 rows a chunk, x 4) * P^T (smem)
+// Both unpackings read the same packed words.  For C a thread owns a row.  For C^T a thread
+// reads the eight bytes of one scale group (16 latents) of four rows, interleaves the nibbles
+// of two rows so that one conversion yields the pair (row, row + 1) of a latent, and stores
+// its 4 x 4 block by a 16x256b tensor-memory store; which latent lands on which lane is free,
+// since O^T's lanes only have to be read back the same way (out_latent).
+//
+// Operands are fp16: code * scale is exact there.  q~ (bf16) is converted once per segment with
+// a power of two per head that puts the head's largest value in [2^14, 2^15): exact unless a
+// value is 2^-31 of the largest or less.  P is p * 2^7 in fp16 (p <= 2^8 under the lazy
+// rescale, so at most 2^15; values below 2^-24 of the row's maximum round to nothing), the row
+// sums stay in fp32 of the unrounded p.
+//
+// Per CTA 20 warps: 0 TMA loads, 1 score MMAs, 2 value MMAs, 3 idle, 4-11 softmax (two
+// warpgroups of 32 heads; they also convert q~ and write the partials), 12-15 unpack C, 16-19
+// unpack C^T.
+#include <math.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "packed.cuh"
+#include "packed_attend.h"
+#include "sm100.cuh"
+#include "split.cuh"
+#include "window.cuh"
+
+namespace mla {
+namespace packed {
+
+constexpr int kTile = 128;                      // rows per tile: two pages
+constexpr int kRawSlots = 3;
+constexpr int kPageCodeBytes = kPageTokens * kCodeBytes;    // 16 KB: two 128-byte halves, 128-byte swizzle
+constexpr int kPageScaleBytes = kPageTokens * kScaleBytes;  // 2 KB
+constexpr int kRawCodeBytes = 2 * kPageCodeBytes;
+constexpr int kRawBytes = kRawCodeBytes + 2 * kPageScaleBytes;  // 36 KB
+constexpr int kQChunkBytes = kHeads * 128;      // 8 KB: 64 heads x 64 latents
+constexpr int kPBytes = kTile * 128;            // 16 KB: 128 rows x 64 heads
+constexpr int kChunks = 8;                      // chunks per tile, of C and of C^T
+constexpr int kStage = 3;                       // operand chunks in tensor memory, each 32 columns
+constexpr int kThreads = 640;
+constexpr int kSoftmaxWarps = 8;
+constexpr float kTau = 8.f;                     // the running max is raised when a score exceeds it by this
+constexpr float kShift = 7.f;                   // P is stored as 2^7 p
+
+constexpr int kOffQ = kRawSlots * kRawBytes;
+constexpr int kOffP = kOffQ + 8 * kQChunkBytes;
+constexpr int kOffRed = kOffP + 2 * kPBytes;    // [4][64] floats
+constexpr int kOffM = kOffRed + 4 * 64 * 4;     // [64] floats: running max less kShift (log2 units)
+constexpr int kOffAlpha = kOffM + 64 * 4;
+constexpr int kOffCs = kOffAlpha + 64 * 4;      // [64] floats: score factor of each head
+constexpr int kOffBar = kOffCs + 64 * 4;
+constexpr int kBarRawFull = 0, kBarRawEmpty = kBarRawFull + kRawSlots, kBarSAFull = kBarRawEmpty + kRawSlots,
+              kBarSAEmpty = kBarSAFull + kStage, kBarVAFull = kBarSAEmpty + kStage,
+              kBarVAEmpty = kBarVAFull + kStage, kBarQFull = kBarVAEmpty + kStage, kBarSFull = kBarQFull + 1,
+              kBarSEmpty = kBarSFull + 1, kBarPFull = kBarSEmpty + 1, kBarPEmpty = kBarPFull + 2,
+              kBarOFull = kBarPEmpty + 2, kBarOEmpty = kBarOFull + 1, kBarDrain = kBarOEmpty + 1,
+              kNumBars = kBarDrain + 1;
+constexpr int kOffMisc = kOffBar + kNumBars * 8;
+constexpr int kSmemBytes = kOffMisc + 16 + 1024;  // slack for 1024-byte alignment of the base
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+// Tensor memory columns.
+constexpr uint32_t kTmemS = 0, kTmemSA = 64, kTmemVA = kTmemSA + 32 * kStage, kTmemO = 256, kTmemCols = 512;
+static_assert(kTmemVA + 32 * kStage <= kTmemO, "tensor memory budget");
+
+using SeqTiles = window::SeqTiles<kTile>;
+using QueryTiles = window::QueryTiles<kTile>;
+
+// Lane L of block mb of O^T holds latent 16 (8 (L / 32) + L % 8) + 4 mb + (L % 32) / 8; a
+// partial is stored in (block, lane) order.  The partial index of latent `lat`:
+__device__ __forceinline__ int partial_index(int lat) {
+  const int grp = lat / kGroup, nib = lat % kGroup;
+  return (nib >> 2) * 128 + (grp >> 3) * 32 + (nib & 3) * 8 + (grp & 7);
+}
+
+// Instruction descriptor, kind::f16 with fp16 A and B and fp32 D.
+constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Tensor-memory store of a 16-lane half quadrant, 32 columns: thread t stores, for column block
+// j of 8, lane base + t/4 in r[4j], r[4j+1] (columns 8j + 2(t%4) and +1) and lane base + t/4 + 8
+// in r[4j+2], r[4j+3].
+__device__ __forceinline__ void tmem_st16x256_x4(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ------------------------------------------------------------------ the tile list
+__device__ __forceinline__ int seq_len(const AttendPackedParams &p, int b) {
+  return min(max(p.a.seq_lens[b], 0), p.a.max_pages * kPageTokens);
+}
+__device__ __forceinline__ int seq_tiles(const AttendPackedParams &p, int b) {
+  return SeqTiles(seq_len(p, b), p.a.Q, p.window, p.sinks).count;
+}
+
+__device__ long long warp_total_tiles(const AttendPackedParams &p, int lane) {
+  long long acc = 0;
+  for (int s = lane; s < p.a.B; s += 32) acc += seq_tiles(p, s);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  return acc;
+}
+
+__device__ void warp_write_seq_prefix(const AttendPackedParams &p, int lane) {
+  long long base = 0;
+  for (int s0 = 0; s0 < p.a.B; s0 += 32) {
+    const int s = s0 + lane;
+    const int nt = s < p.a.B ? seq_tiles(p, s) : 0;
+    long long x = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (s < p.a.B) {
+      p.a.seq_ts[s] = base + x - nt;
+      p.a.seq_nt[s] = nt;
+    }
+    base += __shfl_sync(0xffffffffu, x, 31);
+  }
+}
+
+// Walks the segments (the pieces of sequences) of the list range [t, t_end).  A segment's tiles
+// for this CTA's query are n = first(), then next(n), below hi; none: its partial is empty.
+struct Segment {
+  int b, lo, hi;
+  QueryTiles q;
+  __device__ __forceinline__ int first() const { return q.seek(lo); }
+  __device__ __forceinline__ int next(int n) const { return q.seek(n + 1); }
+};
+struct SegIter {
+  long long t, t_end, base;
+  int s, iq;
+  __device__ SegIter(long long t0, long long t1, int iq_) : t(t0), t_end(t1), base(0), s(0), iq(iq_) {}
+  __device__ bool next(const AttendPackedParams &p, Segment &sg) {
+    if (t >= t_end) return false;
+    int nt = seq_tiles(p, s);
+    while (base + nt <= t) {
+      base += nt;
+      ++s;
+      nt = seq_tiles(p, s);
+    }
+    sg.b = s;
+    sg.q = QueryTiles(seq_len(p, s), p.a.Q, iq, p.window, p.sinks);
+    sg.lo = (int)(t - base);
+    const long long end = min(t_end - base, (long long)nt);
+    sg.hi = min((int)end, sg.q.e);
+    t = base + end;
+    return true;
+  }
+};
+
+// ------------------------------------------------------------------ shared state
+struct Shared {
+  uint8_t *base;
+  uint64_t *bar;
+  float *red, *m, *alpha, *cs;
+  uint32_t *tmem_slot;
+  volatile int *abort_flag;
+};
+
+// A wait of the whole warp.  After an abort (a wait that expired anywhere in the CTA) every
+// wait returns at once and the roles run to their end on whatever they find: shared memory and
+// tensor memory stay theirs, no copy or MMA is issued any more, and *status says so.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, const Shared &sh, int32_t *status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, sh.abort_flag, status));
+}
+
+// A ring position: slot and phase.
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void step(uint32_t n) {
+    if (++slot == n) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// ------------------------------------------------------------------ loads (warp 0, one lane)
+__device__ void producer_role(const AttendPackedParams &p, const Shared &sh, const CUtensorMap *tm_codes,
+                              const CUtensorMap *tm_scales, int iq, long long t0, long long t1) {
+  uint64_t *bar = sh.bar;
+  Ring raw;
+  uint32_t issued = 0;
+  bool ok = true;
+  SegIter it(t0, t1, iq);
+  Segment sg;
+  while (ok && it.next(p, sg)) {
+    for (int n = sg.first(); ok && n < sg.hi; n = sg.next(n)) {
+      ok = mbar_wait(&bar[kBarRawEmpty + raw.slot], raw.phase ^ 1, sh.abort_flag, p.a.status);
+      if (!ok) break;
+      const int j0 = sg.q.seq.tile(n) * kTile;
+      uint8_t *dst = sh.base + raw.slot * kRawBytes;
+      uint64_t *full = &bar[kBarRawFull + raw.slot];
+      // a page without a visible row is not loaded (it need not be mapped)
+      const bool use0 = sg.q.any_row(j0, kPageTokens), use1 = sg.q.any_row(j0 + kPageTokens, kPageTokens);
+      mbar_arrive_expect_tx(full, ((use0 ? 1 : 0) + (use1 ? 1 : 0)) * kPageBytes);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!(h ? use1 : use0)) continue;
+        int page = p.a.page_table[(long long)sg.b * p.a.max_pages + j0 / kPageTokens + h];
+        if (page < 0 || page >= p.a.num_pages) {
+          report_status(p.a.status, kStatusIndex);
+          page = 0;
+        }
+        tma_load_3d(dst + h * kPageCodeBytes, tm_codes, full, 0, page * kPageTokens, 0);
+        tma_load_2d(dst + kRawCodeBytes + h * kPageScaleBytes, tm_scales, full, 0, page * kPageTokens);
+      }
+      raw.step(kRawSlots);
+      ++issued;
+    }
+  }
+  if (!drain_ring(&bar[kBarRawFull], kRawSlots, issued)) report_status(p.a.status, kStatusTimeout);
+}
+
+// ------------------------------------------------------------------ MMA issuers (warps 1 and 2)
+__device__ void score_mma_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, long long t0,
+                               long long t1) {
+  uint64_t *bar = sh.bar;
+  constexpr uint32_t idesc = idesc_f16_f32(kTile, kHeads, false);
+  const uint64_t b0 = sw128_desc(smem_u32(sh.base + kOffQ), 16, 1024);
+  Ring st;
+  uint32_t tiles = 0, segs = 0;
+  SegIter it(t0, t1, iq);
+  Segment sg;
+  while (it.next(p, sg)) {
+    int n = sg.first();
+    if (n >= sg.hi) continue;
+    if (!wait_warp(&bar[kBarQFull], segs & 1, sh, p.a.status)) return;
+    ++segs;
+    for (; n < sg.hi; n = sg.next(n), ++tiles) {
+      if (!wait_warp(&bar[kBarSEmpty], (tiles & 1) ^ 1, sh, p.a.status)) return;
+#pragma unroll 1
+      for (uint32_t ch = 0; ch < kChunks; ++ch) {
+        if (!wait_warp(&bar[kBarSAFull + st.slot], st.phase, sh, p.a.status)) return;
+        tc_fence_after();
+        const uint32_t a = tmem + kTmemSA + st.slot * 32;
+        const uint64_t b = b0 + ch * (kQChunkBytes / 16);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16_tmem_a(tmem + kTmemS, a + kk * 8, b + kk * 2, idesc, (ch != 0 || kk != 0) ? 1u : 0u);
+          umma_commit(&bar[kBarSAEmpty + st.slot]);
+          if (ch == kChunks - 1) umma_commit(&bar[kBarSFull]);
+        }
+        __syncwarp();
+        st.step(kStage);
+      }
+    }
+  }
+}
+
+__device__ void value_mma_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, long long t0,
+                               long long t1) {
+  uint64_t *bar = sh.bar;
+  constexpr uint32_t idesc = idesc_f16_f32(128, kHeads, true);
+  const uint64_t b0 = sw128_desc(smem_u32(sh.base + kOffP), kPBytes, 1024);
+  Ring st;
+  uint32_t tiles = 0, segs = 0;
+  SegIter it(t0, t1, iq);
+  Segment sg;
+  while (it.next(p, sg)) {
+    int n = sg.first();
+    if (n >= sg.hi) continue;
+    if (!wait_warp(&bar[kBarOEmpty], (segs & 1) ^ 1, sh, p.a.status)) return;
+    ++segs;
+    bool fresh = true;
+    while (n < sg.hi) {
+      const int nxt = sg.next(n);
+      if (!wait_warp(&bar[kBarPFull + (tiles & 1)], (tiles >> 1) & 1, sh, p.a.status)) return;
+#pragma unroll 1
+      for (uint32_t ks = 0; ks < kChunks; ++ks) {
+        if (!wait_warp(&bar[kBarVAFull + st.slot], st.phase, sh, p.a.status)) return;
+        tc_fence_after();
+        const uint32_t a = tmem + kTmemVA + st.slot * 32;
+        const uint64_t b = b0 + (tiles & 1) * (kPBytes / 16) + ks * (16 * 128 / 16);
+        const uint32_t acc = (fresh && ks == 0) ? 0u : 1u;
+        if (elect_one()) {
+#pragma unroll
+          for (int mb = 0; mb < 4; ++mb)
+            umma_bf16_tmem_a(tmem + kTmemO + mb * kHeads, a + mb * 8, b, idesc, acc);
+          umma_commit(&bar[kBarVAEmpty + st.slot]);
+          if (ks == kChunks - 1) {
+            umma_commit(&bar[kBarPEmpty + (tiles & 1)]);
+            if (nxt >= sg.hi) umma_commit(&bar[kBarOFull]);
+          }
+        }
+        __syncwarp();
+        st.step(kStage);
+      }
+      fresh = false;
+      n = nxt;
+      ++tiles;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ unpack C (warps 12-15)
+// Thread = row.  A chunk is 64 latents: 32 bytes of codes, four scales, 32 columns.
+__device__ void unpack_rows_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, long long t0,
+                                 long long t1, int wq, int lane) {
+  uint64_t *bar = sh.bar;
+  const int row = wq * 32 + lane;
+  const uint32_t raw0 = smem_u32(sh.base);
+  const uint32_t code_off = (row / kPageTokens) * kPageCodeBytes + (row % kPageTokens) * 128;
+  const uint32_t t_dst = tmem + ((uint32_t)(wq * 32) << 16) + kTmemSA;
+  Ring raw, st;
+  SegIter it(t0, t1, iq);
+  Segment sg;
+  while (it.next(p, sg)) {
+    for (int n = sg.first(); n < sg.hi; n = sg.next(n)) {
+      wait_warp(&bar[kBarRawFull + raw.slot], raw.phase, sh, p.a.status);
+      const uint32_t base = raw0 + raw.slot * kRawBytes;
+      uint32_t sc[8];
+      {
+        const uint4 s0 = ld_shared_v4(base + kRawCodeBytes + row * kScaleBytes);
+        const uint4 s1 = ld_shared_v4(base + kRawCodeBytes + row * kScaleBytes + 16);
+        sc[0] = s0.x, sc[1] = s0.y, sc[2] = s0.z, sc[3] = s0.w;
+        sc[4] = s1.x, sc[5] = s1.y, sc[6] = s1.z, sc[7] = s1.w;
+      }
+#pragma unroll
+      for (int ch = 0; ch < kChunks; ++ch) {
+        const uint32_t half = base + code_off + (ch >> 2) * (kPageTokens * 128);
+        const uint4 w0 = ld_shared_v4(half + (((2 * (ch & 3)) ^ (row & 7)) << 4));
+        const uint4 w1 = ld_shared_v4(half + (((2 * (ch & 3) + 1) ^ (row & 7)) << 4));
+        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        const uint32_t s01 = e4m3x2_to_f16x2(sc[ch] & 0xFFFFu), s23 = e4m3x2_to_f16x2(sc[ch] >> 16);
+        uint32_t r[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // words 2g, 2g + 1 share group g's scale
+          const uint32_t s = prmt(i < 4 ? s01 : s23, 0, (i & 2) ? 0x3232u : 0x1010u);
+          uint32_t v[4];
+          e2m1x8_to_f16x2(w[i], v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) r[4 * i + k] = mul_f16x2(v[k], s);
+        }
+        wait_warp(&bar[kBarSAEmpty + st.slot], st.phase ^ 1, sh, p.a.status);
+        tc_fence_after();
+        tmem_st32(t_dst + st.slot * 32, r);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[kBarSAFull + st.slot]);
+        st.step(kStage);
+      }
+      if (lane == 0) mbar_arrive(&bar[kBarRawEmpty + raw.slot]);
+      raw.step(kRawSlots);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ unpack C^T (warps 16-19)
+// A chunk is 16 rows, the K step of four MMAs.  Thread (warp wq, g = lane / 4, c = lane % 4)
+// owns scale group 8 wq + g of rows 2c, 2c + 1, 2c + 8, 2c + 9 of the chunk, which are K
+// indexes 4c .. 4c + 3: with the rows two apart over c, a half warp's eight-byte loads hit
+// every bank once under the 128-byte swizzle.  (P's rows are stored in the same K order.)
+// Rows the query does not see get the scale zero, so that whatever they hold (a NaN scale, or
+// a page that was not loaded) meets their zero probability as a zero.
+__device__ __forceinline__ int k_of_row(int r) {  // K index of tile row r
+  return (r & ~15) | ((r & 6) << 1) | ((r & 8) >> 2) | (r & 1);
+}
+
+__device__ void unpack_latents_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, long long t0,
+                                    long long t1, int wq, int lane) {
+  uint64_t *bar = sh.bar;
+  const int g = lane >> 2, c = lane & 3;
+  const uint32_t raw0 = smem_u32(sh.base);
+  const int group = 8 * wq + g;
+  // the group's eight bytes in a row: half, 16-byte unit, which eight of it
+  const uint32_t half_off = (wq >> 1) * (kPageTokens * 128);
+  const uint32_t unit = 4 * (wq & 1) + (g >> 1), sub = (g & 1) * 8;
+  const uint32_t t_dst = tmem + ((uint32_t)(wq * 32) << 16) + kTmemVA;
+  Ring raw, st;
+  SegIter it(t0, t1, iq);
+  Segment sg;
+  while (it.next(p, sg)) {
+    for (int n = sg.first(); n < sg.hi; n = sg.next(n)) {
+      wait_warp(&bar[kBarRawFull + raw.slot], raw.phase, sh, p.a.status);
+      const uint32_t base = raw0 + raw.slot * kRawBytes;
+      const int j0 = sg.q.seq.tile(n) * kTile;
+      const bool whole = sg.q.every_row(j0, kTile);
+#pragma unroll 2
+      for (int ks = 0; ks < kChunks; ++ks) {
+        uint2 w[4];
+        uint32_t s[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = 16 * ks + 2 * c + (k & 1) + 8 * (k >> 1);
+          const uint32_t ra = base + (r / kPageTokens) * kPageCodeBytes + half_off + (r % kPageTokens) * 128;
+          w[k] = ld_shared_v2(ra + ((unit ^ (r & 7)) << 4) + sub);
+          s[k] = ld_shared_u8(base + kRawCodeBytes + r * kScaleBytes + group);
+          if (!whole && !sg.q.row(j0 + r)) s[k] = 0;
+        }
+        // r[half of the lanes][4 * block + 2 * upper lanes + column]
+        uint32_t r[2][16];
+#pragma unroll
+        for (int col = 0; col < 2; ++col) {  // rows 2 col, 2 col + 1 of this thread's four
+          const uint32_t sp = e4m3x2_to_f16x2(s[2 * col] | (s[2 * col + 1] << 8));
+#pragma unroll
+          for (int word = 0; word < 2; ++word) {
+            const uint32_t x = word ? w[2 * col].y : w[2 * col].x, y = word ? w[2 * col + 1].y : w[2 * col + 1].x;
+            const uint32_t even = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
+            const uint32_t odd = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
+            uint32_t ve[4], vo[4];
+            e2m1x8_to_f16x2(even, ve);
+            e2m1x8_to_f16x2(odd, vo);
+            // latent 8 word + 2i (even) or + 1 (odd) of the group: block mb = latent / 4,
+            // lane g + 8 (latent % 4)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int mb = 2 * word + (i >> 1), slot = 2 * (i & 1);  // slot: latent % 4 of the even one
+              r[slot >> 1][4 * mb + col] = mul_f16x2(ve[i], sp);
+              r[slot >> 1][4 * mb + 2 + col] = mul_f16x2(vo[i], sp);
+            }
+          }
+        }
+        wait_warp(&bar[kBarVAEmpty + st.slot], st.phase ^ 1, sh, p.a.status);
+        tc_fence_after();
+        tmem_st16x256_x4(t_dst + st.slot * 32, r[0]);
+        tmem_st16x256_x4(t_dst + (16u << 16) + st.slot * 32, r[1]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[kBarVAFull + st.slot]);
+        st.step(kStage);
+      }
+      if (lane == 0) mbar_arrive(&bar[kBarRawEmpty + raw.slot]);
+      raw.step(kRawSlots);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ softmax (warps 4-11)
+// q~ of this segment's query as fp16, K-major with 128-byte swizzle, and the factor that turns
+// an MMA result into a score in log2 units.  Warp w converts heads 8w .. 8w + 7, four at a time.
+__device__ __forceinline__ void convert_query(const AttendPackedParams &p, const Shared &sh, int b, int iq, int w,
+                                              int lane) {
+  const uint16_t *q = p.q_tilde + ((long long)b * p.a.Q + iq) * kHeads * kLatent;
+  const uint32_t dst = smem_u32(sh.base + kOffQ);
+#pragma unroll 1
+  for (int h4 = 0; h4 < 8; h4 += 4) {
+    uint4 v[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        v[i][u] = *reinterpret_cast<const uint4 *>(q + (8 * w + h4 + i) * kLatent + u * 256 + lane * 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int h = 8 * w + h4 + i;
+      uint32_t mx = 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t x[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx = max(mx, max(x[k] & 0x7FFFu, (x[k] >> 16) & 0x7FFFu));
+      }
+      mx = __reduce_max_sync(0xffffffffu, mx);
+      const int e = (int)(mx >> 7);  // the largest value lies in [2^(e - 127), 2^(e - 126))
+      // factor 2^(141 - e) brings it to [2^14, 2^15); a head with an Inf or NaN is left as it is
+      const int f = e == 255 ? 0 : min(141 - e, 126);
+      const float up = __uint_as_float((uint32_t)(127 + f) << 23);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t x[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
+        uint32_t y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = pack_f16x2(bf16lo_to_f32(x[k]) * up, bf16hi_to_f32(x[k]) * up);
+        const uint32_t chunk = 4 * u + (lane >> 3);
+        st_shared_v4(dst + chunk * kQChunkBytes + h * 128 + (((lane & 7) ^ (h & 7)) << 4), y[0], y[1], y[2], y[3]);
+      }
+      if (lane == 0) sh.cs[h] = p.score_factor * __uint_as_float((uint32_t)(127 - f) << 23);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sh.bar[kBarQFull]);
+}
+
+// Reduces each of 32 per-lane columns over the warp: lane l gets column l.
+template <bool kMax>
+__device__ __forceinline__ float reduce_columns(float (&v)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+      const float got = __shfl_xor_sync(0xffffffffu, send, o);
+      v[i] = kMax ? fmaxf(keep, got) : keep + got;
+    }
+  }
+  return v[0];
+}
+
+__device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int grp, int iq,
+                             long long t0, long long t1, int warp, int lane) {
+  uint64_t *bar = sh.bar;
+  const int w = warp - 4, wg = w >> 2, wq = w & 3;
+  const int tid = wq * 32 + lane;    // within the warpgroup
+  const int row = wq * 32 + lane;    // tile row = tensor-memory lane
+  const int col0 = wg * 32;          // heads [col0, col0 + 32)
+  const uint32_t bar_id = 1 + wg;
+  const uint32_t t_lane = tmem + ((uint32_t)(wq * 32) << 16);
+  const int krow = k_of_row(row);
+  const uint32_t p_dst = smem_u32(sh.base + kOffP) + krow * 128;
+  const float4 *cs4 = reinterpret_cast<const float4 *>(sh.cs + col0);
+  const float4 *m4 = reinterpret_cast<const float4 *>(sh.m + col0);
+  uint32_t tiles = 0, segs = 0;
+  SegIter it(t0, t1, iq);
+  Segment sg;
+  while (it.next(p, sg)) {
+    const long long slot = split::partial_slot(p.a, kModePaged, grp, sg.b, iq);
+    int n = sg.first();
+    if (n >= sg.hi) {
+      if (tid < 32) {
+        p.a.part_m[slot * kHeads + col0 + tid] = -INFINITY;
+        p.a.part_l[slot * kHeads + col0 + tid] = 0.f;
+      }
+      continue;
+    }
+    named_bar_sync(3, 32 * kSoftmaxWarps);  // every warp is done with the last segment's factors
+    convert_query(p, sh, sg.b, iq, w, lane);
+    if (tid < 32) sh.m[col0 + tid] = -INFINITY;
+    named_bar_sync(3, 32 * kSoftmaxWarps);
+    float l_part[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) l_part[j] = 0.f;
+    bool first = true;
+    for (; n < sg.hi; n = sg.next(n), ++tiles) {
+      const uint32_t pb = tiles & 1;
+      const int j0 = sg.q.seq.tile(n) * kTile;
+      const bool vis = sg.q.row(j0 + row);
+      mbar_wait(&bar[kBarSFull], tiles & 1, sh.abort_flag, p.a.status);
+      __syncwarp();
+      tc_fence_after();
+      uint32_t s[32];
+      tmem_ld32(t_lane + kTmemS + col0, s);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[kBarSEmpty]);
+      bool flag = first;
+      if (!first) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float4 c4 = cs4[j], mm = m4[j];
+          top = fmaxf(top, fmaf(__uint_as_float(s[4 * j + 0]), c4.x, -mm.x));
+          top = fmaxf(top, fmaf(__uint_as_float(s[4 * j + 1]), c4.y, -mm.y));
+          top = fmaxf(top, fmaf(__uint_as_float(s[4 * j + 2]), c4.z, -mm.z));
+          top = fmaxf(top, fmaf(__uint_as_float(s[4 * j + 3]), c4.w, -mm.w));
+        }
+        flag = vis && top > kTau + kShift;
+      }
+      const bool raise = named_bar_or(bar_id, 128, flag);
+      if (raise) {
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = vis ? fmaxf(__uint_as_float(s[j]) * sh.cs[col0 + j], -INFINITY) : -INFINITY;
+        sh.red[wq * kHeads + col0 + lane] = reduce_columns<true>(v, lane);
+        named_bar_sync(bar_id, 128);
+        if (tid < 32) {
+          const int h = col0 + tid;
+          const float mt = fmaxf(fmaxf(sh.red[h], sh.red[kHeads + h]), fmaxf(sh.red[2 * kHeads + h], sh.red[3 * kHeads + h]));
+          const float mo = sh.m[h];
+          const float mn = fmaxf(mo, mt == -INFINITY ? -1e30f : mt - kShift);
+          sh.alpha[h] = exp2_approx(mo - mn);  // 0 when mo is -inf
+          sh.m[h] = mn;
+        }
+        named_bar_sync(bar_id, 128);
+        if (!first) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) l_part[j] *= sh.alpha[col0 + j];
+        }
+      }
+      uint32_t pw[16];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float4 c4 = cs4[j], mm = m4[j];
+        const float p0 = vis ? exp2_approx(fmaf(__uint_as_float(s[4 * j + 0]), c4.x, -mm.x)) : 0.f;
+        const float p1 = vis ? exp2_approx(fmaf(__uint_as_float(s[4 * j + 1]), c4.y, -mm.y)) : 0.f;
+        const float p2 = vis ? exp2_approx(fmaf(__uint_as_float(s[4 * j + 2]), c4.z, -mm.z)) : 0.f;
+        const float p3 = vis ? exp2_approx(fmaf(__uint_as_float(s[4 * j + 3]), c4.w, -mm.w)) : 0.f;
+        l_part[4 * j + 0] += p0;
+        l_part[4 * j + 1] += p1;
+        l_part[4 * j + 2] += p2;
+        l_part[4 * j + 3] += p3;
+        pw[2 * j] = pack_f16x2(p0, p1);
+        pw[2 * j + 1] = pack_f16x2(p2, p3);
+      }
+      // this P buffer is free (the value MMAs of two tiles ago are done)
+      mbar_wait(&bar[kBarPEmpty + pb], ((tiles >> 1) & 1) ^ 1, sh.abort_flag, p.a.status);
+      if (raise && !first) {
+        // the running max moved: once the last tile's value MMAs are done, rescale O^T
+        mbar_wait(&bar[kBarPEmpty + (pb ^ 1)], ((tiles - 1) >> 1) & 1, sh.abort_flag, p.a.status);
+        __syncwarp();
+        tc_fence_after();
+#pragma unroll 1
+        for (int mb = 0; mb < 4; ++mb) {
+          uint32_t o[32];
+          const uint32_t addr = t_lane + kTmemO + mb * kHeads + col0;
+          tmem_ld32(addr, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sh.alpha[col0 + j]);
+          tmem_st32(addr, o);
+        }
+        tmem_st_wait();
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        st_shared_v4(p_dst + pb * kPBytes + (((4 * wg + u) ^ (krow & 7)) << 4), pw[4 * u], pw[4 * u + 1], pw[4 * u + 2],
+                     pw[4 * u + 3]);
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[kBarPFull + pb]);
+      first = false;
+    }
+    // ---- epilogue: the partial (O, m, l)
+    sh.red[wq * kHeads + col0 + lane] = reduce_columns<false>(l_part, lane);
+    named_bar_sync(bar_id, 128);
+    if (tid < 32) {
+      const int h = col0 + tid;
+      p.a.part_m[slot * kHeads + h] = sh.m[h];
+      p.a.part_l[slot * kHeads + h] = sh.red[h] + sh.red[kHeads + h] + sh.red[2 * kHeads + h] + sh.red[3 * kHeads + h];
+    }
+    mbar_wait(&bar[kBarOFull], segs & 1, sh.abort_flag, p.a.status);
+    __syncwarp();
+    tc_fence_after();
+    float *po = p.a.part_o + slot * kHeads * kLatent;
+#pragma unroll 1
+    for (int mb = 0; mb < 4; ++mb) {
+      uint32_t o[32];
+      tmem_ld32(t_lane + kTmemO + mb * kHeads + col0, o);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) po[(col0 + j) * kLatent + mb * 128 + row] = __uint_as_float(o[j]);
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[kBarOEmpty]);
+    ++segs;
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_packed_kernel(const __grid_constant__ CUtensorMap tm_codes, const __grid_constant__ CUtensorMap tm_scales,
+                         const AttendPackedParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  Shared sh;
+  sh.base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  sh.bar = reinterpret_cast<uint64_t *>(sh.base + kOffBar);
+  sh.red = reinterpret_cast<float *>(sh.base + kOffRed);
+  sh.m = reinterpret_cast<float *>(sh.base + kOffM);
+  sh.alpha = reinterpret_cast<float *>(sh.base + kOffAlpha);
+  sh.cs = reinterpret_cast<float *>(sh.base + kOffCs);
+  sh.tmem_slot = reinterpret_cast<uint32_t *>(sh.base + kOffMisc);
+  sh.abort_flag = reinterpret_cast<volatile int *>(sh.base + kOffMisc + 4);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int g = blockIdx.x / p.a.group_size, iq = blockIdx.x % p.a.group_size;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRawSlots; ++i) {
+      mbar_init(&sh.bar[kBarRawFull + i], 1);
+      mbar_init(&sh.bar[kBarRawEmpty + i], 8);
+    }
+    for (int i = 0; i < kStage; ++i) {
+      mbar_init(&sh.bar[kBarSAFull + i], 4);
+      mbar_init(&sh.bar[kBarSAEmpty + i], 1);
+      mbar_init(&sh.bar[kBarVAFull + i], 4);
+      mbar_init(&sh.bar[kBarVAEmpty + i], 1);
+    }
+    mbar_init(&sh.bar[kBarQFull], kSoftmaxWarps);
+    mbar_init(&sh.bar[kBarSFull], 1);
+    mbar_init(&sh.bar[kBarSEmpty], kSoftmaxWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.bar[kBarPFull + i], kSoftmaxWarps);
+      mbar_init(&sh.bar[kBarPEmpty + i], 1);
+    }
+    mbar_init(&sh.bar[kBarOFull], 1);
+    mbar_init(&sh.bar[kBarOEmpty], kSoftmaxWarps);
+    mbar_init(&sh.bar[kBarDrain], 2);
+    *sh.abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&tm_codes);
+    prefetch_tensormap(&tm_scales);
+  }
+  if (warp == 1) {
+    tmem_alloc(sh.tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  grid_dep_launch();
+  grid_dep_wait();  // everything below may come from the previous kernel
+  const long long T = warp_total_tiles(p, lane);
+  const long long G = p.a.groups;
+  if (blockIdx.x == 0 && warp == 3) warp_write_seq_prefix(p, lane);
+  const long long t0 = split::group_start(g, T, G), t1 = split::group_start(g + 1, T, G);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *sh.tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) producer_role(p, sh, &tm_codes, &tm_scales, iq, t0, t1);
+  } else if (warp == 1) {
+    score_mma_role(p, sh, tmem, iq, t0, t1);
+  } else if (warp == 2) {
+    value_mma_role(p, sh, tmem, iq, t0, t1);
+  } else if (warp >= 16) {
+    unpack_latents_role(p, sh, tmem, iq, t0, t1, warp & 3, lane);
+  } else if (warp >= 12) {
+    unpack_rows_role(p, sh, tmem, iq, t0, t1, warp & 3, lane);
+  } else if (warp >= 4) {
+    softmax_role(p, sh, tmem, g, iq, t0, t1, warp, lane);
+  }
+
+  __syncwarp();
+  // After an abort the MMAs already issued must finish before tensor memory is released.
+  if (warp == 2 && *sh.abort_flag) {
+    if (lane == 0) umma_commit(&sh.bar[kBarDrain]);
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    if (*sh.abort_flag) {
+      if (lane == 0) {
+        umma_commit(&sh.bar[kBarDrain]);
+        if (!mbar_wait_drain(&sh.bar[kBarDrain], 0)) report_status(p.a.status, kStatusTimeout);
+      }
+      __syncwarp();
+    }
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ combine
+// One block per (query row, two heads); thread t merges latents 4t .. 4t + 3 of both from the
+// row's partials: with M the largest running max, O = sum 2^(m_k - M) O_k and l likewise, then
+// unit * O / l and lse = (M + log2 l) ln 2.  A partial is in (block, lane) order: the four
+// values of a thread are four words apart by eight, and a warp's loads cover whole sectors.
+constexpr int kCombineHeads = 2, kCombineChunk = 3;
+
+__global__ void __launch_bounds__(128, 8) combine_packed_kernel(const AttendPackedParams p) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int v = blockIdx.x, b = v / p.a.Q, i = v % p.a.Q, tid = threadIdx.x;
+  __shared__ split::GroupRange sh_gr;
+  if (tid == 0) {
+    sh_gr = split::seq_group_range(p.a, kModePaged, b);
+    if (blockIdx.y == 0 && i == 0) {
+      const int L = p.a.seq_lens[b];
+      if (L < 0 || L > p.a.max_pages * kPageTokens) report_status(p.a.status, kStatusIndex);
+    }
+  }
+  __syncthreads();
+  const split::GroupRange gr = sh_gr;
+  const int h0 = blockIdx.y * kCombineHeads;
+  const int idx = partial_index(4 * tid);
+  float M[kCombineHeads], den[kCombineHeads], acc[kCombineHeads][4];
+#pragma unroll
+  for (int hh = 0; hh < kCombineHeads; ++hh) {
+    M[hh] = -INFINITY;
+    den[hh] = acc[hh][0] = acc[hh][1] = acc[hh][2] = acc[hh][3] = 0.f;
+  }
+  for (int k0 = 0; k0 < gr.count; k0 += kCombineChunk) {
+    float mk[kCombineHeads][kCombineChunk], lk[kCombineHeads][kCombineChunk], ok[kCombineHeads][kCombineChunk][4];
+#pragma unroll
+    for (int j = 0; j < kCombineChunk; ++j) {
+      const int k = k0 + j;
+      const bool live = k < gr.count;
+      const long long slot = live ? split::partial_slot(p.a, kModePaged, gr.partial_group(k), b, i) : 0;
+#pragma unroll
+      for (int hh = 0; hh < kCombineHeads; ++hh) {
+        const long long r = slot * kHeads + h0 + hh;
+        mk[hh][j] = live ? p.a.part_m[r] : -INFINITY;
+        lk[hh][j] = live ? p.a.part_l[r] : 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ok[hh][j][e] = live ? p.a.part_o[r * kLatent + idx + 8 * e] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int hh = 0; hh < kCombineHeads; ++hh) {
+      float mx = M[hh];
+#pragma unroll
+      for (int j = 0; j < kCombineChunk; ++j) mx = fmaxf(mx, mk[hh][j]);
+      if (mx == -INFINITY) continue;
+      const float a = exp2f(M[hh] - mx);  // 0 when M was -inf
+      den[hh] *= a;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[hh][e] *= a;
+#pragma unroll
+      for (int j = 0; j < kCombineChunk; ++j) {
+        if (mk[hh][j] == -INFINITY) continue;  // an empty partial's O was never written
+        const float wt = exp2f(mk[hh][j] - mx);
+        den[hh] += wt * lk[hh][j];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[hh][e] += wt * ok[hh][j][e];
+      }
+      M[hh] = mx;
+    }
+  }
+#pragma unroll
+  for (int hh = 0; hh < kCombineHeads; ++hh) {
+    const bool seen = M[hh] != -INFINITY;
+    const float inv = seen ? p.unit / den[hh] : 0.f;
+    uint2 out;
+    out.x = pack_bf16x2(acc[hh][0] * inv, acc[hh][1] * inv);
+    out.y = pack_bf16x2(acc[hh][2] * inv, acc[hh][3] * inv);
+    *reinterpret_cast<uint2 *>(p.a.o_latent + ((long long)v * kHeads + h0 + hh) * kLatent + 4 * tid) = out;
+    if (p.a.lse != nullptr && tid == 0)
+      p.a.lse[(long long)v * kHeads + h0 + hh] = seen ? (M[hh] + log2f(den[hh])) * 0.69314718055994530942f : -INFINITY;
+  }
+}
+
+}  // namespace packed
+
+cudaError_t launch_attend_packed(const CUtensorMap &tm_codes, const CUtensorMap &tm_scales, const AttendPackedParams &p,
+                                 cudaStream_t stream) {
+  static std::atomic<int> configured_device{-1};
+  if (cudaError_t e = set_smem_limit_once(packed::attend_packed_kernel, packed::kSmemBytes, configured_device);
+      e != cudaSuccess)
+    return e;
+  if (cudaError_t e = launch_chained(packed::attend_packed_kernel, dim3(p.a.groups * p.a.group_size),
+                                     dim3(packed::kThreads), packed::kSmemBytes, stream, tm_codes, tm_scales, p);
+      e != cudaSuccess)
+    return e;
+  return launch_chained(packed::combine_packed_kernel, dim3(p.a.B * p.a.Q, kHeads / packed::kCombineHeads), dim3(128), 0,
+                        stream, p);
+}
+
+}  // namespace mla

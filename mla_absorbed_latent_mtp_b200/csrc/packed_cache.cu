@@ -1,0 +1,236 @@
+// packed_cache.cu -- the 4-bit paged latent cache (packed.cuh): quantising append, read-back,
+// truncation.  The lengths and errors behave as in cache.cu.
+//
+// Append: 16 latents, one scale group, per thread, a row per warp: 32 bytes in, 8 + 1 out.
+//   y = x / unit,  s = e4m3(max|y| / 6),  code = e2m1(y / s)
+// The divisions are IEEE divisions: a value on the border between two codes (y / s exactly
+// 0.25, 0.75, ...) has to meet the conversion as a tie, which a product with a rounded 1 / s
+// does not give.  unit is a power of two, so y is exact.
+#include <algorithm>
+
+#include "internal.h"
+#include "mla.h"
+#include "packed.cuh"
+#include "sm100.cuh"
+
+namespace mla {
+namespace packed {
+
+constexpr int kThreads = 256;
+constexpr int kRowsPerPass = kThreads / 32;
+constexpr int kRowsPerCta = 64;  // rows of a sequence that one CTA appends when there are many
+
+struct Store {
+  uint8_t *pool;
+  const int32_t *page_table;
+  int max_pages, num_pages;
+};
+
+// Byte offset of position j of sequence b, or -1 if it has no slot.
+__device__ __forceinline__ long long row_offset(const Store &st, int b, long long j) {
+  if (j < 0 || j >= (long long)st.max_pages * kPageTokens) return -1;
+  const int page = st.page_table[(long long)b * st.max_pages + j / kPageTokens];
+  if (page < 0 || page >= st.num_pages) return -1;
+  return ((long long)page * kPageTokens + j % kPageTokens) * kRowBytes;
+}
+
+// Positions [lo, hi) of sequence b all have slots (the whole block takes part).
+__device__ bool range_ok(const Store &st, int b, long long lo, long long hi) {
+  bool ok = lo >= 0 && hi <= (long long)st.max_pages * kPageTokens;
+  if (ok)
+    for (long long pg = lo / kPageTokens + threadIdx.x; pg * kPageTokens < hi; pg += blockDim.x)
+      ok = ok && row_offset(st, b, pg * kPageTokens) >= 0;
+  return __syncthreads_and(ok);
+}
+
+__device__ __forceinline__ void append_group(const uint16_t *src, uint8_t *row, int group, float inv_unit) {
+  uint32_t x[8];
+  {
+    const uint4 a = *reinterpret_cast<const uint4 *>(src + group * kGroup);
+    const uint4 b = *reinterpret_cast<const uint4 *>(src + group * kGroup + 8);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  uint32_t mx = 0;  // the largest |x|, as bf16 bits
+#pragma unroll
+  for (int k = 0; k < 8; ++k) mx = max(mx, max(x[k] & 0x7FFFu, (x[k] >> 16) & 0x7FFFu));
+  const float amax = __uint_as_float(mx << 16) * inv_unit;
+  uint2 codes = make_uint2(0u, 0u);
+  uint32_t scale = 0x7Fu;  // NaN: a group with an Inf or a NaN reads back as NaN
+  if (mx < 0x7F80u) {
+    scale = f32_to_e4m3x2(__fdiv_rn(amax, 6.f), 0.f) & 0xFFu;
+    const float s = __half2float(__ushort_as_half((unsigned short)(e4m3x2_to_f16x2(scale) & 0xFFFFu)));
+    if (s > 0.f) {
+      float v[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[2 * k] = __fdiv_rn(bf16lo_to_f32(x[4 * h + k]) * inv_unit, s);
+          v[2 * k + 1] = __fdiv_rn(bf16hi_to_f32(x[4 * h + k]) * inv_unit, s);
+        }
+        (h ? codes.y : codes.x) = f32x8_to_e2m1(v);
+      }
+    }
+  }
+  *reinterpret_cast<uint2 *>(row + group * 8) = codes;
+  row[kCodeBytes + group] = (uint8_t)scale;
+}
+
+// CTA (b, y) appends rows [y * rows_per_cta, + rows_per_cta) of sequence b.  With one CTA per
+// sequence it also advances the length; with more, finish_append_kernel does once all have read it.
+__global__ void __launch_bounds__(kThreads) append_kernel(const Store st, int32_t *seq_lens, const uint16_t *rows,
+                                                          int Q, int rows_per_cta, float inv_unit, int32_t *status) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int b = blockIdx.x;
+  const long long L = seq_lens[b];
+  const bool ok = range_ok(st, b, L, L + Q) && L >= 0;
+  const int i0 = blockIdx.y * rows_per_cta, i1 = min(Q, i0 + rows_per_cta);
+  if (ok) {
+    const int lane = threadIdx.x & 31;
+    for (int i = i0 + (int)(threadIdx.x >> 5); i < i1; i += kRowsPerPass)
+      append_group(rows + ((long long)b * Q + i) * kLatent, st.pool + row_offset(st, b, L + i), lane, inv_unit);
+  }
+  if (gridDim.y == 1) {
+    __syncthreads();  // every thread has read the length
+    if (threadIdx.x == 0) {
+      if (ok) seq_lens[b] = (int32_t)(L + Q);
+      else report_status(status, kStatusIndex);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) finish_append_kernel(const Store st, int32_t *seq_lens, int Q,
+                                                                 int32_t *status) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int b = blockIdx.x;
+  const long long L = seq_lens[b];
+  const bool ok = range_ok(st, b, L, L + Q) && L >= 0;
+  if (threadIdx.x == 0) {
+    if (ok) seq_lens[b] = (int32_t)(L + Q);
+    else report_status(status, kStatusIndex);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) truncate_kernel(const Store st, int32_t *seq_lens, const int32_t *keep,
+                                                            int Q, int32_t *status) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int b = blockIdx.x;
+  const long long L = seq_lens[b], k = keep[b], new_len = L - Q + k;
+  const bool ok = range_ok(st, b, new_len, L) && k >= 0 && k <= Q && L - Q >= 0;
+  if (ok) {
+    constexpr int kUnits = kRowBytes / 16;
+    const long long n = (L - new_len) * kUnits;
+    for (long long x = threadIdx.x; x < n; x += kThreads)
+      *reinterpret_cast<uint4 *>(st.pool + row_offset(st, b, new_len + x / kUnits) + x % kUnits * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    if (ok) seq_lens[b] = (int32_t)new_len;
+    else report_status(status, kStatusIndex);
+  }
+}
+
+// rows[b, i] = the values at position start[b] + i, 16 latents per thread.
+__global__ void __launch_bounds__(kThreads) unpack_kernel(const Store st, const int32_t *start, uint16_t *rows, int B,
+                                                          int n, float unit, int32_t *status) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int group = threadIdx.x & 31;
+  const long long total = (long long)B * n;
+  for (long long r = (long long)blockIdx.x * kRowsPerPass + (threadIdx.x >> 5); r < total;
+       r += (long long)gridDim.x * kRowsPerPass) {
+    const int b = (int)(r / n), i = (int)(r % n);
+    const long long off = start[b] < 0 ? -1 : row_offset(st, b, (long long)start[b] + i);
+    uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (off < 0) {
+      if (group == 0) report_status(status, kStatusIndex);
+    } else {
+      const uint2 w = *reinterpret_cast<const uint2 *>(st.pool + off + group * 8);
+      const uint32_t s = prmt(e4m3x2_to_f16x2(st.pool[off + kCodeBytes + group]), 0, 0x1010u);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t v[4];
+        e2m1x8_to_f16x2(h ? w.y : w.x, v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t y = mul_f16x2(v[k], s);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&y));
+          out[4 * h + k] = pack_bf16x2(f.x * unit, f.y * unit);
+        }
+      }
+    }
+    uint4 *dst = reinterpret_cast<uint4 *>(rows + r * kLatent + group * kGroup);
+    dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+  }
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+mla_status check(const void *pool, const int32_t *page_table, const void *lens, const void *x, int B, int Q, int R,
+                 int page_size, int max_pages, int num_pages, float unit) {
+  if (pool == nullptr || page_table == nullptr || lens == nullptr || x == nullptr || B < 1 || Q < 1) return MLA_ERR_ARG;
+  if (max_pages < 1 || num_pages < 1 || !valid_unit(unit)) return MLA_ERR_ARG;
+  if (R != kLatent || page_size != kPageTokens || !aligned16(pool) || !aligned16(x)) return MLA_ERR_UNSUPPORTED;
+  if ((long long)max_pages * kPageTokens >= (1LL << 31)) return MLA_ERR_ARG;  // positions are int32
+  if ((long long)num_pages * kPageTokens >= (1LL << 31)) return MLA_ERR_ARG;
+  return MLA_OK;
+}
+
+}  // namespace packed
+}  // namespace mla
+
+extern "C" {
+
+mla_status mla_cache_append_packed(uint8_t *pool, const int32_t *page_table, int32_t *seq_lens, const uint16_t *rows,
+                                   int B, int Q, int R, int page_size, int max_pages, int num_pages, float unit,
+                                   int32_t *status, void *stream) {
+  using namespace mla;
+  using namespace mla::packed;
+  if (mla_status s = check(pool, page_table, seq_lens, rows, B, Q, R, page_size, max_pages, num_pages, unit);
+      s != MLA_OK)
+    return s;
+  const int splits = (Q + kRowsPerCta - 1) / kRowsPerCta;
+  if (splits > 65535) return MLA_ERR_ARG;  // grid limit
+  const Store st{pool, page_table, max_pages, num_pages};
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_chained(append_kernel, dim3(B, splits), dim3(kThreads), 0, cs, st, seq_lens, rows, Q,
+                                 kRowsPerCta, 1.f / unit, status);
+  if (e == cudaSuccess && splits > 1)
+    e = launch_chained(finish_append_kernel, dim3(B), dim3(kThreads), 0, cs, st, seq_lens, Q, status);
+  return record_cuda_error(e);
+}
+
+mla_status mla_cache_truncate_packed(uint8_t *pool, const int32_t *page_table, int32_t *seq_lens, const int32_t *keep,
+                                     int B, int Q, int R, int page_size, int max_pages, int num_pages,
+                                     int32_t *status, void *stream) {
+  using namespace mla;
+  using namespace mla::packed;
+  if (keep == nullptr) return MLA_ERR_ARG;
+  if (mla_status s = check(pool, page_table, seq_lens, pool, B, Q, R, page_size, max_pages, num_pages, 1.f); s != MLA_OK)
+    return s;
+  const Store st{pool, page_table, max_pages, num_pages};
+  return record_cuda_error(launch_chained(truncate_kernel, dim3(B), dim3(kThreads), 0,
+                                          reinterpret_cast<cudaStream_t>(stream), st, seq_lens, keep, Q, status));
+}
+
+mla_status mla_cache_unpack(const uint8_t *pool, const int32_t *page_table, const int32_t *start, uint16_t *rows, int B,
+                            int n, int R, int page_size, int max_pages, int num_pages, float unit, int32_t *status,
+                            void *stream) {
+  using namespace mla;
+  using namespace mla::packed;
+  if (mla_status s = check(pool, page_table, start, rows, B, n, R, page_size, max_pages, num_pages, unit); s != MLA_OK)
+    return s;
+  const Store st{const_cast<uint8_t *>(pool), page_table, max_pages, num_pages};
+  const long long ctas = ((long long)B * n + kRowsPerPass - 1) / kRowsPerPass;
+  const int grid = (int)std::min<long long>(ctas, 16LL * device_sm_count());
+  return record_cuda_error(launch_chained(unpack_kernel, dim3(grid), dim3(kThreads), 0,
+                                          reinterpret_cast<cudaStream_t>(stream), st, start, rows, B, n, unit, status));
+}
+
+}  // extern "C"

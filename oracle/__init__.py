@@ -334,3 +334,79 @@ def kpool_select(pooled: np.ndarray, w: np.ndarray, pos: int, pool: int, topk: i
         tail = list(range(n_sel * pool, pos + 1))
         out += tail + [-1] * (pool - 1 - len(tail))
     return np.asarray(out, dtype=np.int32)
+
+
+# ----------------------------------------------------------------------------- sliding windows
+def window_positions(L_b: int, q_len: int, i: int, window: int, sinks: int) -> np.ndarray:
+    """Positions that query i sees: j <= t with t - j < window or j < sinks (window 0: all j <= t)."""
+    j = np.arange(max(L_b - q_len + i + 1, 0))
+    if window == 0:
+        return j
+    t = L_b - q_len + i
+    return j[(t - j < window) | (j < sinks)]
+
+
+def attend_rows(qt: np.ndarray, rows: np.ndarray, scale: float = 1.0 / 16.0):
+    """One query: qt [H, R], rows [n, R] (float64) -> o [H, R], lse [H], and sum_j a_j |c_j| [H, R]
+    (what a relative error of the weights is multiplied by)."""
+    if rows.shape[0] == 0:
+        zero = np.zeros_like(qt)
+        return zero, np.full(qt.shape[0], -np.inf), zero
+    s = (qt @ rows.T) * scale
+    top = s.max(axis=1, keepdims=True)
+    e = np.exp(s - top)
+    total = e.sum(axis=1, keepdims=True)
+    a = e / total
+    return a @ rows, (top + np.log(total))[:, 0], a @ np.abs(rows)
+
+
+# ----------------------------------------------------------------------------- the 4-bit row
+E2M1_VALUES = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+PACKED_GROUP = 16
+
+
+def e4m3_value(b) -> np.ndarray:
+    """Values of e4m3 bytes (1 sign, 4 exponent bits of bias 7, 3 fraction bits; 0x7F is NaN)."""
+    b = np.asarray(b, dtype=np.int64)
+    e, f = (b >> 3) & 15, b & 7
+    v = np.where(e == 0, f * 2.0 ** -9, (1 + f / 8.0) * np.exp2(e - 7.0))
+    v = np.where((b & 0x7F) == 0x7F, np.nan, v)
+    return np.where(b & 0x80, -v, v)
+
+
+_E4M3 = None
+
+
+def _nearest_even(x: np.ndarray, grid: np.ndarray) -> np.ndarray:
+    """Index into the ascending grid of the nearest value, ties to the even index, ends saturating."""
+    hi = np.clip(np.searchsorted(grid, x), 1, len(grid) - 1)
+    lo = hi - 1
+    below, above = x - grid[lo], grid[hi] - x
+    return np.where(below < above, lo, np.where(above < below, hi, np.where(lo % 2 == 0, lo, hi)))
+
+
+def packed_quantise(rows: np.ndarray, unit: float = 1.0) -> np.ndarray:
+    """rows [..., 512] float64 -> bytes [..., 288]: e2m1 codes (even latent in the low nibble), then
+    one e4m3 scale per 16 latents."""
+    global _E4M3
+    if _E4M3 is None:
+        _E4M3 = e4m3_value(np.arange(0x7F))  # 0 .. 448, ascending
+    y = (rows / unit).reshape(rows.shape[:-1] + (rows.shape[-1] // PACKED_GROUP, PACKED_GROUP))
+    finite = np.isfinite(y).all(axis=-1)
+    y = np.where(finite[..., None], y, 0.0)
+    scale = _nearest_even(np.abs(y).max(axis=-1) / 6.0, _E4M3)
+    s = _E4M3[scale][..., None]
+    q = np.divide(y, s, out=np.zeros_like(y), where=s > 0)
+    code = _nearest_even(np.abs(q), E2M1_VALUES) + 8 * np.signbit(q)
+    code = code.reshape(rows.shape).astype(np.uint8)
+    packed = code[..., 0::2] | (code[..., 1::2] << 4)
+    return np.concatenate([packed, np.where(finite, scale, 0x7F).astype(np.uint8)], axis=-1)
+
+
+def packed_values(packed: np.ndarray, unit: float = 1.0) -> np.ndarray:
+    """bytes [..., 288] -> values [..., 512] float64."""
+    c = packed[..., :256].astype(np.int64)
+    code = np.stack([c & 15, c >> 4], axis=-1).reshape(c.shape[:-1] + (512,))
+    v = np.where(code & 8, -1.0, 1.0) * E2M1_VALUES[code & 7]
+    s = np.repeat(e4m3_value(packed[..., 256:]), PACKED_GROUP, axis=-1)
+    return v * s * unit
