@@ -26,9 +26,9 @@
 // rescale, so at most 2^15; values below 2^-24 of the row's maximum round to nothing), the row
 // sums stay in fp32 of the unrounded p.
 //
-// Per CTA 20 warps: 0 TMA loads, 1 score MMAs, 2 value MMAs, 3 idle, 4-11 softmax (two
-// warpgroups of 32 heads; they also convert q~ and write the partials), 12-15 unpack C, 16-19
-// unpack C^T.
+// Per CTA 19 warps (five on a scheduler: 96 registers a thread): 0 TMA loads, 1 score MMAs, 2 value
+// MMAs, 3-10 softmax (two groups of four warps, 32 heads each; they also convert q~ and write
+// the partials), 11-14 unpack C, 15-18 unpack C^T.
 #include <math.h>
 
 #include <algorithm>
@@ -53,7 +53,7 @@ constexpr int kQChunkBytes = kHeads * 128;      // 8 KB: 64 heads x 64 latents
 constexpr int kPBytes = kTile * 128;            // 16 KB: 128 rows x 64 heads
 constexpr int kChunks = 8;                      // chunks per tile, of C and of C^T
 constexpr int kStage = 3;                       // operand chunks in tensor memory, each 32 columns
-constexpr int kThreads = 640;
+constexpr int kThreads = 608;
 constexpr int kSoftmaxWarps = 8;
 constexpr float kTau = 8.f;                     // the running max is raised when a score exceeds it by this
 constexpr float kShift = 7.f;                   // P is stored as 2^7 p
@@ -63,7 +63,8 @@ constexpr int kOffP = kOffQ + 8 * kQChunkBytes;
 constexpr int kOffRed = kOffP + 2 * kPBytes;    // [4][64] floats
 constexpr int kOffM = kOffRed + 4 * 64 * 4;     // [64] floats: running max less kShift (log2 units)
 constexpr int kOffAlpha = kOffM + 64 * 4;
-constexpr int kOffCs = kOffAlpha + 64 * 4;      // [64] floats: score factor of each head
+constexpr int kOffRise = kOffAlpha + 64 * 4;
+constexpr int kOffCs = kOffRise + 64 * 4;      // [64] floats: score factor of each head
 constexpr int kOffBar = kOffCs + 64 * 4;
 constexpr int kBarRawFull = 0, kBarRawEmpty = kBarRawFull + kRawSlots, kBarSAFull = kBarRawEmpty + kRawSlots,
               kBarSAEmpty = kBarSAFull + kStage, kBarVAFull = kBarSAEmpty + kStage,
@@ -113,6 +114,11 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
 __device__ __forceinline__ uint2 ld_shared_v2(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
 }
 __device__ __forceinline__ uint32_t ld_shared_u8(uint32_t a) {
@@ -168,6 +174,9 @@ struct Segment {
   QueryTiles q;
   __device__ __forceinline__ int first() const { return q.seek(lo); }
   __device__ __forceinline__ int next(int n) const { return q.seek(n + 1); }
+  __device__ __forceinline__ int count() const {
+    return max(min(hi, q.a) - lo, 0) + max(hi - max(lo, q.b), 0);
+  }
 };
 struct SegIter {
   long long t, t_end, base;
@@ -195,7 +204,7 @@ struct SegIter {
 struct Shared {
   uint8_t *base;
   uint64_t *bar;
-  float *red, *m, *alpha, *cs;
+  float *red, *m, *alpha, *rise, *cs;
   uint32_t *tmem_slot;
   volatile int *abort_flag;
 };
@@ -266,11 +275,11 @@ __device__ void score_mma_role(const AttendPackedParams &p, const Shared &sh, ui
   SegIter it(t0, t1, iq);
   Segment sg;
   while (it.next(p, sg)) {
-    int n = sg.first();
-    if (n >= sg.hi) continue;
+    const int count = sg.count();
+    if (count == 0) continue;
     if (!wait_warp(&bar[kBarQFull], segs & 1, sh, p.a.status)) return;
     ++segs;
-    for (; n < sg.hi; n = sg.next(n), ++tiles) {
+    for (int k = 0; k < count; ++k, ++tiles) {
       if (!wait_warp(&bar[kBarSEmpty], (tiles & 1) ^ 1, sh, p.a.status)) return;
 #pragma unroll 1
       for (uint32_t ch = 0; ch < kChunks; ++ch) {
@@ -302,13 +311,11 @@ __device__ void value_mma_role(const AttendPackedParams &p, const Shared &sh, ui
   SegIter it(t0, t1, iq);
   Segment sg;
   while (it.next(p, sg)) {
-    int n = sg.first();
-    if (n >= sg.hi) continue;
+    const int count = sg.count();
+    if (count == 0) continue;
     if (!wait_warp(&bar[kBarOEmpty], (segs & 1) ^ 1, sh, p.a.status)) return;
     ++segs;
-    bool fresh = true;
-    while (n < sg.hi) {
-      const int nxt = sg.next(n);
+    for (int k = 0; k < count; ++k, ++tiles) {
       if (!wait_warp(&bar[kBarPFull + (tiles & 1)], (tiles >> 1) & 1, sh, p.a.status)) return;
 #pragma unroll 1
       for (uint32_t ks = 0; ks < kChunks; ++ks) {
@@ -316,7 +323,7 @@ __device__ void value_mma_role(const AttendPackedParams &p, const Shared &sh, ui
         tc_fence_after();
         const uint32_t a = tmem + kTmemVA + st.slot * 32;
         const uint64_t b = b0 + (tiles & 1) * (kPBytes / 16) + ks * (16 * 128 / 16);
-        const uint32_t acc = (fresh && ks == 0) ? 0u : 1u;
+        const uint32_t acc = (k == 0 && ks == 0) ? 0u : 1u;
         if (elect_one()) {
 #pragma unroll
           for (int mb = 0; mb < 4; ++mb)
@@ -324,20 +331,47 @@ __device__ void value_mma_role(const AttendPackedParams &p, const Shared &sh, ui
           umma_commit(&bar[kBarVAEmpty + st.slot]);
           if (ks == kChunks - 1) {
             umma_commit(&bar[kBarPEmpty + (tiles & 1)]);
-            if (nxt >= sg.hi) umma_commit(&bar[kBarOFull]);
+            if (k == count - 1) umma_commit(&bar[kBarOFull]);
           }
         }
         __syncwarp();
         st.step(kStage);
       }
-      fresh = false;
-      n = nxt;
-      ++tiles;
     }
   }
 }
 
-// ------------------------------------------------------------------ unpack C (warps 12-15)
+// ------------------------------------------------------------------ unpack C (warps 11-14)
+// Both unpackers run one chunk behind themselves: the next chunk's words are read from shared
+// memory before this one's are converted (the last chunk reads the first again, to no use), and a chunk is handed to the MMA warp only after the
+// next one has been converted, when its tensor-memory store is long done.  The chunk loops stay
+// rolled: with five kinds of warps on a scheduler, unrolled bodies missed the instruction cache
+// (32 x 8,192 rows: 117 us with the chunks unrolled).
+struct Stager {
+  uint64_t *full, *empty;
+  Ring st;
+  uint32_t pending;  // slot whose store is in flight, or kNone
+  static constexpr uint32_t kNone = ~0u;
+  __device__ __forceinline__ void hand_over(int lane) {
+    if (pending == kNone) return;
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&full[pending]);
+    pending = kNone;
+  }
+  // Waits until the MMAs that read the slot's last chunk are done.
+  __device__ __forceinline__ uint32_t acquire(const Shared &sh, int32_t *status) {
+    wait_warp(&empty[st.slot], st.phase ^ 1, sh, status);
+    tc_fence_after();
+    return st.slot;
+  }
+  __device__ __forceinline__ void stored() {
+    pending = st.slot;
+    st.step(kStage);
+  }
+};
+
 // Thread = row.  A chunk is 64 latents: 32 bytes of codes, four scales, 32 columns.
 __device__ void unpack_rows_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, long long t0,
                                  long long t1, int wq, int lane) {
@@ -346,27 +380,28 @@ __device__ void unpack_rows_role(const AttendPackedParams &p, const Shared &sh, 
   const uint32_t raw0 = smem_u32(sh.base);
   const uint32_t code_off = (row / kPageTokens) * kPageCodeBytes + (row % kPageTokens) * 128;
   const uint32_t t_dst = tmem + ((uint32_t)(wq * 32) << 16) + kTmemSA;
-  Ring raw, st;
+  Ring raw;
+  Stager out{&bar[kBarSAFull], &bar[kBarSAEmpty], Ring(), Stager::kNone};
   SegIter it(t0, t1, iq);
   Segment sg;
   while (it.next(p, sg)) {
     for (int n = sg.first(); n < sg.hi; n = sg.next(n)) {
       wait_warp(&bar[kBarRawFull + raw.slot], raw.phase, sh, p.a.status);
       const uint32_t base = raw0 + raw.slot * kRawBytes;
-      uint32_t sc[8];
-      {
-        const uint4 s0 = ld_shared_v4(base + kRawCodeBytes + row * kScaleBytes);
-        const uint4 s1 = ld_shared_v4(base + kRawCodeBytes + row * kScaleBytes + 16);
-        sc[0] = s0.x, sc[1] = s0.y, sc[2] = s0.z, sc[3] = s0.w;
-        sc[4] = s1.x, sc[5] = s1.y, sc[6] = s1.z, sc[7] = s1.w;
-      }
-#pragma unroll
-      for (int ch = 0; ch < kChunks; ++ch) {
+      uint4 w0, w1;
+      uint32_t sc;
+      auto load = [&](int ch) {
         const uint32_t half = base + code_off + (ch >> 2) * (kPageTokens * 128);
-        const uint4 w0 = ld_shared_v4(half + (((2 * (ch & 3)) ^ (row & 7)) << 4));
-        const uint4 w1 = ld_shared_v4(half + (((2 * (ch & 3) + 1) ^ (row & 7)) << 4));
+        w0 = ld_shared_v4(half + (((2 * (ch & 3)) ^ (row & 7)) << 4));
+        w1 = ld_shared_v4(half + (((2 * (ch & 3) + 1) ^ (row & 7)) << 4));
+        sc = ld_shared_u32(base + kRawCodeBytes + row * kScaleBytes + 4 * ch);
+      };
+      load(0);
+#pragma unroll 1
+      for (int ch = 0; ch < kChunks; ++ch) {
         const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-        const uint32_t s01 = e4m3x2_to_f16x2(sc[ch] & 0xFFFFu), s23 = e4m3x2_to_f16x2(sc[ch] >> 16);
+        const uint32_t s01 = e4m3x2_to_f16x2(sc & 0xFFFFu), s23 = e4m3x2_to_f16x2(sc >> 16);
+        load((ch + 1) % kChunks);
         uint32_t r[32];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {  // words 2g, 2g + 1 share group g's scale
@@ -376,22 +411,18 @@ __device__ void unpack_rows_role(const AttendPackedParams &p, const Shared &sh, 
 #pragma unroll
           for (int k = 0; k < 4; ++k) r[4 * i + k] = mul_f16x2(v[k], s);
         }
-        wait_warp(&bar[kBarSAEmpty + st.slot], st.phase ^ 1, sh, p.a.status);
-        tc_fence_after();
-        tmem_st32(t_dst + st.slot * 32, r);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[kBarSAFull + st.slot]);
-        st.step(kStage);
+        out.hand_over(lane);
+        tmem_st32(t_dst + out.acquire(sh, p.a.status) * 32, r);
+        out.stored();
       }
       if (lane == 0) mbar_arrive(&bar[kBarRawEmpty + raw.slot]);
       raw.step(kRawSlots);
+      out.hand_over(lane);
     }
   }
 }
 
-// ------------------------------------------------------------------ unpack C^T (warps 16-19)
+// ------------------------------------------------------------------ unpack C^T (warps 15-18)
 // A chunk is 16 rows, the K step of four MMAs.  Thread (warp wq, g = lane / 4, c = lane % 4)
 // owns scale group 8 wq + g of rows 2c, 2c + 1, 2c + 8, 2c + 9 of the chunk, which are K
 // indexes 4c .. 4c + 3: with the rows two apart over c, a half warp's eight-byte loads hit
@@ -406,13 +437,17 @@ __device__ void unpack_latents_role(const AttendPackedParams &p, const Shared &s
                                     long long t1, int wq, int lane) {
   uint64_t *bar = sh.bar;
   const int g = lane >> 2, c = lane & 3;
-  const uint32_t raw0 = smem_u32(sh.base);
   const int group = 8 * wq + g;
-  // the group's eight bytes in a row: half, 16-byte unit, which eight of it
-  const uint32_t half_off = (wq >> 1) * (kPageTokens * 128);
-  const uint32_t unit = 4 * (wq & 1) + (g >> 1), sub = (g & 1) * 8;
+  // the group's eight bytes in a row: half, 16-byte unit, which eight of it; the thread's rows of
+  // a chunk are 2c + b + 8h, whose unit is the same for both h
+  const uint32_t unit = 4 * (wq & 1) + (g >> 1);
+  const uint32_t off0 = (wq >> 1) * (kPageTokens * 128) + (g & 1) * 8 + (2 * c) * 128;
+  const uint32_t row_off[2] = {off0 + ((unit ^ (2 * c)) << 4), off0 + 128 + ((unit ^ (2 * c + 1)) << 4)};
+  const uint32_t scale_off = kRawCodeBytes + (2 * c) * kScaleBytes + group;
+  const uint32_t raw0 = smem_u32(sh.base);
   const uint32_t t_dst = tmem + ((uint32_t)(wq * 32) << 16) + kTmemVA;
-  Ring raw, st;
+  Ring raw;
+  Stager out{&bar[kBarVAFull], &bar[kBarVAEmpty], Ring(), Stager::kNone};
   SegIter it(t0, t1, iq);
   Segment sg;
   while (it.next(p, sg)) {
@@ -421,26 +456,35 @@ __device__ void unpack_latents_role(const AttendPackedParams &p, const Shared &s
       const uint32_t base = raw0 + raw.slot * kRawBytes;
       const int j0 = sg.q.seq.tile(n) * kTile;
       const bool whole = sg.q.every_row(j0, kTile);
-#pragma unroll 2
-      for (int ks = 0; ks < kChunks; ++ks) {
-        uint2 w[4];
-        uint32_t s[4];
+      uint2 w[4];
+      uint32_t s[4];
+      auto load = [&](int ks) {
+        const uint32_t page = base + (ks >> 2) * kPageCodeBytes + (ks & 3) * (16 * 128);
+        const uint32_t sp = base + scale_off + ks * 16 * kScaleBytes;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = 16 * ks + 2 * c + (k & 1) + 8 * (k >> 1);
-          const uint32_t ra = base + (r / kPageTokens) * kPageCodeBytes + half_off + (r % kPageTokens) * 128;
-          w[k] = ld_shared_v2(ra + ((unit ^ (r & 7)) << 4) + sub);
-          s[k] = ld_shared_u8(base + kRawCodeBytes + r * kScaleBytes + group);
-          if (!whole && !sg.q.row(j0 + r)) s[k] = 0;
+        for (int k = 0; k < 4; ++k) {  // row 2c + k % 2 + 8 (k / 2)
+          w[k] = ld_shared_v2(page + row_off[k & 1] + (k >> 1) * (8 * 128));
+          s[k] = ld_shared_u8(sp + ((k & 1) + 8 * (k >> 1)) * kScaleBytes);
         }
-        // r[half of the lanes][4 * block + 2 * upper lanes + column]
+      };
+      load(0);
+#pragma unroll 1
+      for (int ks = 0; ks < kChunks; ++ks) {
+        if (!whole) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (!sg.q.row(j0 + 16 * ks + 2 * c + (k & 1) + 8 * (k >> 1))) s[k] = 0;
+        }
+        // r[upper 16 lanes][4 * block + 2 * upper 8 lanes + column]
         uint32_t r[2][16];
+        const uint32_t sp[2] = {e4m3x2_to_f16x2(prmt(s[0], s[1], 0x0040u)), e4m3x2_to_f16x2(prmt(s[2], s[3], 0x0040u))};
+        const uint2 v[4] = {w[0], w[1], w[2], w[3]};
+        load((ks + 1) % kChunks);
 #pragma unroll
         for (int col = 0; col < 2; ++col) {  // rows 2 col, 2 col + 1 of this thread's four
-          const uint32_t sp = e4m3x2_to_f16x2(s[2 * col] | (s[2 * col + 1] << 8));
 #pragma unroll
           for (int word = 0; word < 2; ++word) {
-            const uint32_t x = word ? w[2 * col].y : w[2 * col].x, y = word ? w[2 * col + 1].y : w[2 * col + 1].x;
+            const uint32_t x = word ? v[2 * col].y : v[2 * col].x, y = word ? v[2 * col + 1].y : v[2 * col + 1].x;
             const uint32_t even = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u);
             const uint32_t odd = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
             uint32_t ve[4], vo[4];
@@ -451,28 +495,25 @@ __device__ void unpack_latents_role(const AttendPackedParams &p, const Shared &s
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int mb = 2 * word + (i >> 1), slot = 2 * (i & 1);  // slot: latent % 4 of the even one
-              r[slot >> 1][4 * mb + col] = mul_f16x2(ve[i], sp);
-              r[slot >> 1][4 * mb + 2 + col] = mul_f16x2(vo[i], sp);
+              r[slot >> 1][4 * mb + col] = mul_f16x2(ve[i], sp[col]);
+              r[slot >> 1][4 * mb + 2 + col] = mul_f16x2(vo[i], sp[col]);
             }
           }
         }
-        wait_warp(&bar[kBarVAEmpty + st.slot], st.phase ^ 1, sh, p.a.status);
-        tc_fence_after();
-        tmem_st16x256_x4(t_dst + st.slot * 32, r[0]);
-        tmem_st16x256_x4(t_dst + (16u << 16) + st.slot * 32, r[1]);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[kBarVAFull + st.slot]);
-        st.step(kStage);
+        out.hand_over(lane);
+        const uint32_t dst = t_dst + out.acquire(sh, p.a.status) * 32;
+        tmem_st16x256_x4(dst, r[0]);
+        tmem_st16x256_x4(dst + (16u << 16), r[1]);
+        out.stored();
       }
       if (lane == 0) mbar_arrive(&bar[kBarRawEmpty + raw.slot]);
       raw.step(kRawSlots);
+      out.hand_over(lane);
     }
   }
 }
 
-// ------------------------------------------------------------------ softmax (warps 4-11)
+// ------------------------------------------------------------------ softmax (warps 3-10)
 // q~ of this segment's query as fp16, K-major with 128-byte swizzle, and the factor that turns
 // an MMA result into a score in log2 units.  Warp w converts heads 8w .. 8w + 7, four at a time.
 __device__ __forceinline__ void convert_query(const AttendPackedParams &p, const Shared &sh, int b, int iq, int w,
@@ -519,17 +560,15 @@ __device__ __forceinline__ void convert_query(const AttendPackedParams &p, const
   if (lane == 0) mbar_arrive(&sh.bar[kBarQFull]);
 }
 
-// Reduces each of 32 per-lane columns over the warp: lane l gets column l.
-template <bool kMax>
-__device__ __forceinline__ float reduce_columns(float (&v)[32], int lane) {
+// Sums each of 32 per-lane columns over the warp: lane l gets column l.
+__device__ __forceinline__ float sum_columns(float (&v)[32], int lane) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const bool up = (lane & o) != 0;
 #pragma unroll
     for (int i = 0; i < o; ++i) {
       const float send = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
-      const float got = __shfl_xor_sync(0xffffffffu, send, o);
-      v[i] = kMax ? fmaxf(keep, got) : keep + got;
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
     }
   }
   return v[0];
@@ -538,7 +577,7 @@ __device__ __forceinline__ float reduce_columns(float (&v)[32], int lane) {
 __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int grp, int iq,
                              long long t0, long long t1, int warp, int lane) {
   uint64_t *bar = sh.bar;
-  const int w = warp - 4, wg = w >> 2, wq = w & 3;
+  const int w = warp - 3, wg = w >> 2, wq = warp & 3;
   const int tid = wq * 32 + lane;    // within the warpgroup
   const int row = wq * 32 + lane;    // tile row = tensor-memory lane
   const int col0 = wg * 32;          // heads [col0, col0 + 32)
@@ -563,7 +602,7 @@ __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint
     }
     named_bar_sync(3, 32 * kSoftmaxWarps);  // every warp is done with the last segment's factors
     convert_query(p, sh, sg.b, iq, w, lane);
-    if (tid < 32) sh.m[col0 + tid] = -INFINITY;
+    if (tid < 32) sh.m[col0 + tid] = 0.f;
     named_bar_sync(3, 32 * kSoftmaxWarps);
     float l_part[32];
 #pragma unroll
@@ -576,60 +615,64 @@ __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint
       mbar_wait(&bar[kBarSFull], tiles & 1, sh.abort_flag, p.a.status);
       __syncwarp();
       tc_fence_after();
-      uint32_t s[32];
-      tmem_ld32(t_lane + kTmemS + col0, s);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[kBarSEmpty]);
-      bool flag = first;
-      if (!first) {
-        float top = -INFINITY;
+      float x[32];  // score - m, in log2 units
+      {
+        uint32_t s[32];
+        tmem_ld32(t_lane + kTmemS + col0, s);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[kBarSEmpty]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float4 c4 = cs4[j], mm = m4[j];
-          top = fmaxf(top, fmaf(__uint_as_float(s[4 * j + 0]), c4.x, -mm.x));
-          top = fmaxf(top, fmaf(__uint_as_float(s[4 * j + 1]), c4.y, -mm.y));
-          top = fmaxf(top, fmaf(__uint_as_float(s[4 * j + 2]), c4.z, -mm.z));
-          top = fmaxf(top, fmaf(__uint_as_float(s[4 * j + 3]), c4.w, -mm.w));
+          x[4 * j + 0] = fmaf(__uint_as_float(s[4 * j + 0]), c4.x, -mm.x);
+          x[4 * j + 1] = fmaf(__uint_as_float(s[4 * j + 1]), c4.y, -mm.y);
+          x[4 * j + 2] = fmaf(__uint_as_float(s[4 * j + 2]), c4.z, -mm.z);
+          x[4 * j + 3] = fmaf(__uint_as_float(s[4 * j + 3]), c4.w, -mm.w);
         }
-        flag = vis && top > kTau + kShift;
       }
-      const bool raise = named_bar_or(bar_id, 128, flag);
-      if (raise) {
-        float v[32];
+      if (!vis) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = vis ? fmaxf(__uint_as_float(s[j]) * sh.cs[col0 + j], -INFINITY) : -INFINITY;
-        sh.red[wq * kHeads + col0 + lane] = reduce_columns<true>(v, lane);
+        for (int j = 0; j < 32; ++j) x[j] = -INFINITY;
+      }
+      float top = x[0];
+#pragma unroll
+      for (int j = 1; j < 32; ++j) top = fmaxf(top, x[j]);
+      const bool raise = named_bar_or(bar_id, 128, first || top > kTau + kShift);
+      if (raise) {
+        int mine = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const int i = __float_as_int(fmaxf(x[j], -INFINITY));  // a NaN does not count
+          const int best = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7FFFFFFF));  // ordered as the floats
+          if (lane == j) mine = best ^ ((best >> 31) & 0x7FFFFFFF);
+        }
+        sh.red[wq * kHeads + col0 + lane] = __int_as_float(mine);
         named_bar_sync(bar_id, 128);
         if (tid < 32) {
           const int h = col0 + tid;
           const float mt = fmaxf(fmaxf(sh.red[h], sh.red[kHeads + h]), fmaxf(sh.red[2 * kHeads + h], sh.red[3 * kHeads + h]));
-          const float mo = sh.m[h];
-          const float mn = fmaxf(mo, mt == -INFINITY ? -1e30f : mt - kShift);
-          sh.alpha[h] = exp2_approx(mo - mn);  // 0 when mo is -inf
-          sh.m[h] = mn;
+          float d = mt - kShift;  // how far m rises (the first tile sets it)
+          if (mt == -INFINITY || (!first && d < 0.f)) d = 0.f;
+          sh.rise[h] = d;
+          sh.alpha[h] = exp2_approx(-d);
+          sh.m[h] += d;
         }
         named_bar_sync(bar_id, 128);
-        if (!first) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) l_part[j] *= sh.alpha[col0 + j];
+        for (int j = 0; j < 32; ++j) {
+          x[j] -= sh.rise[col0 + j];
+          if (!first) l_part[j] *= sh.alpha[col0 + j];
         }
       }
       uint32_t pw[16];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float4 c4 = cs4[j], mm = m4[j];
-        const float p0 = vis ? exp2_approx(fmaf(__uint_as_float(s[4 * j + 0]), c4.x, -mm.x)) : 0.f;
-        const float p1 = vis ? exp2_approx(fmaf(__uint_as_float(s[4 * j + 1]), c4.y, -mm.y)) : 0.f;
-        const float p2 = vis ? exp2_approx(fmaf(__uint_as_float(s[4 * j + 2]), c4.z, -mm.z)) : 0.f;
-        const float p3 = vis ? exp2_approx(fmaf(__uint_as_float(s[4 * j + 3]), c4.w, -mm.w)) : 0.f;
-        l_part[4 * j + 0] += p0;
-        l_part[4 * j + 1] += p1;
-        l_part[4 * j + 2] += p2;
-        l_part[4 * j + 3] += p3;
-        pw[2 * j] = pack_f16x2(p0, p1);
-        pw[2 * j + 1] = pack_f16x2(p2, p3);
+      for (int j = 0; j < 16; ++j) {
+        const float p0 = exp2_approx(x[2 * j]), p1 = exp2_approx(x[2 * j + 1]);
+        l_part[2 * j] += p0;
+        l_part[2 * j + 1] += p1;
+        pw[j] = pack_f16x2(p0, p1);
       }
       // this P buffer is free (the value MMAs of two tiles ago are done)
       mbar_wait(&bar[kBarPEmpty + pb], ((tiles >> 1) & 1) ^ 1, sh.abort_flag, p.a.status);
@@ -661,7 +704,7 @@ __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint
       first = false;
     }
     // ---- epilogue: the partial (O, m, l)
-    sh.red[wq * kHeads + col0 + lane] = reduce_columns<false>(l_part, lane);
+    sh.red[wq * kHeads + col0 + lane] = sum_columns(l_part, lane);
     named_bar_sync(bar_id, 128);
     if (tid < 32) {
       const int h = col0 + tid;
@@ -698,6 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   sh.red = reinterpret_cast<float *>(sh.base + kOffRed);
   sh.m = reinterpret_cast<float *>(sh.base + kOffM);
   sh.alpha = reinterpret_cast<float *>(sh.base + kOffAlpha);
+  sh.rise = reinterpret_cast<float *>(sh.base + kOffRise);
   sh.cs = reinterpret_cast<float *>(sh.base + kOffCs);
   sh.tmem_slot = reinterpret_cast<uint32_t *>(sh.base + kOffMisc);
   sh.abort_flag = reinterpret_cast<volatile int *>(sh.base + kOffMisc + 4);
@@ -739,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_wait();  // everything below may come from the previous kernel
   const long long T = warp_total_tiles(p, lane);
   const long long G = p.a.groups;
-  if (blockIdx.x == 0 && warp == 3) warp_write_seq_prefix(p, lane);
+  if (blockIdx.x == 0 && warp == 0) warp_write_seq_prefix(p, lane);
   const long long t0 = split::group_start(g, T, G), t1 = split::group_start(g + 1, T, G);
   tc_fence_before();
   __syncthreads();
@@ -752,11 +796,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     score_mma_role(p, sh, tmem, iq, t0, t1);
   } else if (warp == 2) {
     value_mma_role(p, sh, tmem, iq, t0, t1);
-  } else if (warp >= 16) {
+  } else if (warp >= 15) {
     unpack_latents_role(p, sh, tmem, iq, t0, t1, warp & 3, lane);
-  } else if (warp >= 12) {
+  } else if (warp >= 11) {
     unpack_rows_role(p, sh, tmem, iq, t0, t1, warp & 3, lane);
-  } else if (warp >= 4) {
+  } else {
     softmax_role(p, sh, tmem, g, iq, t0, t1, warp, lane);
   }
 
