@@ -220,11 +220,11 @@ static mla_status attend_packed_common(const uint16_t *q_tilde, const uint8_t *p
     return MLA_ERR_WORKSPACE;
   CUtensorMap tm_codes, tm_scales;
   {
-    // a row's 256 code bytes as two halves of 128: one box {128 bytes, 64 rows, 2} is a page's codes
+    // a row's 256 code bytes as two halves of 128: one box {128 bytes, 64 rows, 1} is half a page's codes
     const uint64_t rows = (uint64_t)num_pages * kPageTokens;
     const uint64_t dims[3] = {128, rows, 2};
     const uint64_t strides[2] = {packed::kRowBytes, 128};
-    const uint32_t box[3] = {128, kPageTokens, 2};
+    const uint32_t box[3] = {128, kPageTokens, 1};
     if (!make_bytes_map(&tm_codes, pool, 3, dims, strides, box, true)) return cuda_status(cudaErrorInvalidValue);
     const uint64_t sdims[2] = {packed::kScaleBytes, rows};
     const uint32_t sbox[2] = {packed::kScaleBytes, kPageTokens};

@@ -45,9 +45,9 @@ namespace packed {
 
 constexpr int kTile = 128;                      // rows per tile: two pages
 constexpr int kRawSlots = 3;
-constexpr int kPageCodeBytes = kPageTokens * kCodeBytes;    // 16 KB: two 128-byte halves, 128-byte swizzle
+constexpr int kHalfBytes = kTile * 128;                     // 16 KB: 128 rows of 128 code bytes, 128-byte swizzle
 constexpr int kPageScaleBytes = kPageTokens * kScaleBytes;  // 2 KB
-constexpr int kRawCodeBytes = 2 * kPageCodeBytes;
+constexpr int kRawCodeBytes = 2 * kHalfBytes;
 constexpr int kRawBytes = kRawCodeBytes + 2 * kPageScaleBytes;  // 36 KB
 constexpr int kQChunkBytes = kHeads * 128;      // 8 KB: 64 heads x 64 latents
 constexpr int kPBytes = kTile * 128;            // 16 KB: 128 rows x 64 heads
@@ -61,7 +61,7 @@ constexpr float kShift = 7.f;                   // P is stored as 2^7 p
 constexpr int kOffQ = kRawSlots * kRawBytes;
 constexpr int kOffP = kOffQ + 8 * kQChunkBytes;
 constexpr int kOffRed = kOffP + 2 * kPBytes;    // [4][64] floats
-constexpr int kOffM = kOffRed + 4 * 64 * 4;     // [64] floats: running max less kShift (log2 units)
+constexpr int kOffM = kOffRed + 4 * 64 * 4;     // [64] floats: kShift less the running max (log2 units)
 constexpr int kOffAlpha = kOffM + 64 * 4;
 constexpr int kOffRise = kOffAlpha + 64 * 4;
 constexpr int kOffCs = kOffRise + 64 * 4;      // [64] floats: score factor of each head
@@ -130,6 +130,20 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Pairs of floats in one instruction: d = a b + c, d += a.
+__device__ __forceinline__ void fma_f32x2(float &d0, float &d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void add_f32x2(float &d0, float &d1, float a0, float a1) {
+  asm("{\n\t.reg .b64 a, d;\n\tmov.b64 d, {%0, %1};\n\tmov.b64 a, {%2, %3};\n\tadd.rn.f32x2 d, d, a;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1));
 }
 
 // ------------------------------------------------------------------ the tile list
@@ -209,11 +223,39 @@ struct Shared {
   volatile int *abort_flag;
 };
 
-// A wait of the whole warp.  After an abort (a wait that expired anywhere in the CTA) every
-// wait returns at once and the roles run to their end on whatever they find: shared memory and
+// Barriers are addressed by their shared-memory address and index.  A wait is one probe on the
+// fast path; what follows a failed probe is out of line, since the roles' code competes for the
+// instruction cache.  After an abort (a wait that expired anywhere in the CTA) every wait
+// returns at once and the roles run to their end on whatever they find: shared memory and
 // tensor memory stay theirs, no copy or MMA is issued any more, and *status says so.
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, const Shared &sh, int32_t *status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, sh.abort_flag, status));
+struct Bars {
+  uint32_t addr;
+  volatile int *abort_flag;
+  int32_t *status;
+  __device__ __forceinline__ uint32_t operator[](uint32_t i) const { return addr + 8 * i; }
+};
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *status) {
+  const long long t0 = clock64();
+  while (true) {
+    if (*abort_flag) return false;
+    if (mbar_try_wait_sleep(bar, parity, 1000000u)) return true;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      *abort_flag = 1;
+      report_status(status, kStatusTimeout);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool wait(const Bars &bar, uint32_t i, uint32_t parity) {
+  if (mbar_test_wait(bar[i], parity)) return true;
+  return wait_slow(bar[i], parity, bar.abort_flag, bar.status);
+}
+// The same for a converged warp: true if it completed for every lane.
+__device__ __forceinline__ bool wait_warp(const Bars &bar, uint32_t i, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait(bar, i, parity));
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(bar) : "memory");
 }
 
 // A ring position: slot and phase.
@@ -254,7 +296,8 @@ __device__ void producer_role(const AttendPackedParams &p, const Shared &sh, con
           report_status(p.a.status, kStatusIndex);
           page = 0;
         }
-        tma_load_3d(dst + h * kPageCodeBytes, tm_codes, full, 0, page * kPageTokens, 0);
+        tma_load_3d(dst + h * (kHalfBytes / 2), tm_codes, full, 0, page * kPageTokens, 0);
+        tma_load_3d(dst + kHalfBytes + h * (kHalfBytes / 2), tm_codes, full, 0, page * kPageTokens, 1);
         tma_load_2d(dst + kRawCodeBytes + h * kPageScaleBytes, tm_scales, full, 0, page * kPageTokens);
       }
       raw.step(kRawSlots);
@@ -267,7 +310,7 @@ __device__ void producer_role(const AttendPackedParams &p, const Shared &sh, con
 // ------------------------------------------------------------------ MMA issuers (warps 1 and 2)
 __device__ void score_mma_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, long long t0,
                                long long t1) {
-  uint64_t *bar = sh.bar;
+  const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.a.status};
   constexpr uint32_t idesc = idesc_f16_f32(kTile, kHeads, false);
   const uint64_t b0 = sw128_desc(smem_u32(sh.base + kOffQ), 16, 1024);
   Ring st;
@@ -277,13 +320,13 @@ __device__ void score_mma_role(const AttendPackedParams &p, const Shared &sh, ui
   while (it.next(p, sg)) {
     const int count = sg.count();
     if (count == 0) continue;
-    if (!wait_warp(&bar[kBarQFull], segs & 1, sh, p.a.status)) return;
+    if (!wait_warp(bar, kBarQFull, segs & 1)) return;
     ++segs;
     for (int k = 0; k < count; ++k, ++tiles) {
-      if (!wait_warp(&bar[kBarSEmpty], (tiles & 1) ^ 1, sh, p.a.status)) return;
+      if (!wait_warp(bar, kBarSEmpty, (tiles & 1) ^ 1)) return;
 #pragma unroll 1
       for (uint32_t ch = 0; ch < kChunks; ++ch) {
-        if (!wait_warp(&bar[kBarSAFull + st.slot], st.phase, sh, p.a.status)) return;
+        if (!wait_warp(bar, kBarSAFull + st.slot, st.phase)) return;
         tc_fence_after();
         const uint32_t a = tmem + kTmemSA + st.slot * 32;
         const uint64_t b = b0 + ch * (kQChunkBytes / 16);
@@ -291,8 +334,8 @@ __device__ void score_mma_role(const AttendPackedParams &p, const Shared &sh, ui
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             umma_bf16_tmem_a(tmem + kTmemS, a + kk * 8, b + kk * 2, idesc, (ch != 0 || kk != 0) ? 1u : 0u);
-          umma_commit(&bar[kBarSAEmpty + st.slot]);
-          if (ch == kChunks - 1) umma_commit(&bar[kBarSFull]);
+          umma_commit(&sh.bar[kBarSAEmpty + st.slot]);
+          if (ch == kChunks - 1) umma_commit(&sh.bar[kBarSFull]);
         }
         __syncwarp();
         st.step(kStage);
@@ -303,7 +346,7 @@ __device__ void score_mma_role(const AttendPackedParams &p, const Shared &sh, ui
 
 __device__ void value_mma_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, long long t0,
                                long long t1) {
-  uint64_t *bar = sh.bar;
+  const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.a.status};
   constexpr uint32_t idesc = idesc_f16_f32(128, kHeads, true);
   const uint64_t b0 = sw128_desc(smem_u32(sh.base + kOffP), kPBytes, 1024);
   Ring st;
@@ -313,13 +356,13 @@ __device__ void value_mma_role(const AttendPackedParams &p, const Shared &sh, ui
   while (it.next(p, sg)) {
     const int count = sg.count();
     if (count == 0) continue;
-    if (!wait_warp(&bar[kBarOEmpty], (segs & 1) ^ 1, sh, p.a.status)) return;
+    if (!wait_warp(bar, kBarOEmpty, (segs & 1) ^ 1)) return;
     ++segs;
     for (int k = 0; k < count; ++k, ++tiles) {
-      if (!wait_warp(&bar[kBarPFull + (tiles & 1)], (tiles >> 1) & 1, sh, p.a.status)) return;
+      if (!wait_warp(bar, kBarPFull + (tiles & 1), (tiles >> 1) & 1)) return;
 #pragma unroll 1
       for (uint32_t ks = 0; ks < kChunks; ++ks) {
-        if (!wait_warp(&bar[kBarVAFull + st.slot], st.phase, sh, p.a.status)) return;
+        if (!wait_warp(bar, kBarVAFull + st.slot, st.phase)) return;
         tc_fence_after();
         const uint32_t a = tmem + kTmemVA + st.slot * 32;
         const uint64_t b = b0 + (tiles & 1) * (kPBytes / 16) + ks * (16 * 128 / 16);
@@ -328,10 +371,10 @@ __device__ void value_mma_role(const AttendPackedParams &p, const Shared &sh, ui
 #pragma unroll
           for (int mb = 0; mb < 4; ++mb)
             umma_bf16_tmem_a(tmem + kTmemO + mb * kHeads, a + mb * 8, b, idesc, acc);
-          umma_commit(&bar[kBarVAEmpty + st.slot]);
+          umma_commit(&sh.bar[kBarVAEmpty + st.slot]);
           if (ks == kChunks - 1) {
-            umma_commit(&bar[kBarPEmpty + (tiles & 1)]);
-            if (k == count - 1) umma_commit(&bar[kBarOFull]);
+            umma_commit(&sh.bar[kBarPEmpty + (tiles & 1)]);
+            if (k == count - 1) umma_commit(&sh.bar[kBarOFull]);
           }
         }
         __syncwarp();
@@ -342,32 +385,26 @@ __device__ void value_mma_role(const AttendPackedParams &p, const Shared &sh, ui
 }
 
 // ------------------------------------------------------------------ unpack C (warps 11-14)
-// Both unpackers run one chunk behind themselves: the next chunk's words are read from shared
-// memory before this one's are converted (the last chunk reads the first again, to no use), and a chunk is handed to the MMA warp only after the
-// next one has been converted, when its tensor-memory store is long done.  The chunk loops stay
-// rolled: with five kinds of warps on a scheduler, unrolled bodies missed the instruction cache
-// (32 x 8,192 rows: 117 us with the chunks unrolled).
+// Both unpackers read the next chunk's words from shared memory before they convert this one's
+// (the last chunk reads the first again, to no use).  The chunk loops stay rolled: with five kinds
+// of warps on a scheduler, unrolled bodies missed the instruction cache (32 x 8,192 rows: 117 us
+// with the chunks unrolled).
 struct Stager {
-  uint64_t *full, *empty;
+  Bars bar;
+  uint32_t full, empty;  // barrier indexes of slot 0
   Ring st;
-  uint32_t pending;  // slot whose store is in flight, or kNone
-  static constexpr uint32_t kNone = ~0u;
-  __device__ __forceinline__ void hand_over(int lane) {
-    if (pending == kNone) return;
-    tmem_st_wait();
-    tc_fence_before();
+  // The slot, once the MMAs that read its last chunk are done.
+  __device__ __forceinline__ uint32_t acquire() {
+    wait(bar, empty + st.slot, st.phase ^ 1);
     __syncwarp();
-    if (lane == 0) mbar_arrive(&full[pending]);
-    pending = kNone;
-  }
-  // Waits until the MMAs that read the slot's last chunk are done.
-  __device__ __forceinline__ uint32_t acquire(const Shared &sh, int32_t *status) {
-    wait_warp(&empty[st.slot], st.phase ^ 1, sh, status);
     tc_fence_after();
     return st.slot;
   }
-  __device__ __forceinline__ void stored() {
-    pending = st.slot;
+  __device__ __forceinline__ void hand_over(int lane) {
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) arrive(bar[full + st.slot]);
     st.step(kStage);
   }
 };
@@ -375,25 +412,26 @@ struct Stager {
 // Thread = row.  A chunk is 64 latents: 32 bytes of codes, four scales, 32 columns.
 __device__ void unpack_rows_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, long long t0,
                                  long long t1, int wq, int lane) {
-  uint64_t *bar = sh.bar;
+  const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.a.status};
   const int row = wq * 32 + lane;
   const uint32_t raw0 = smem_u32(sh.base);
-  const uint32_t code_off = (row / kPageTokens) * kPageCodeBytes + (row % kPageTokens) * 128;
+  const uint32_t code_off = row * 128 + ((row & 7) << 4);
   const uint32_t t_dst = tmem + ((uint32_t)(wq * 32) << 16) + kTmemSA;
   Ring raw;
-  Stager out{&bar[kBarSAFull], &bar[kBarSAEmpty], Ring(), Stager::kNone};
+  Stager out{bar, kBarSAFull, kBarSAEmpty, Ring()};
   SegIter it(t0, t1, iq);
   Segment sg;
   while (it.next(p, sg)) {
     for (int n = sg.first(); n < sg.hi; n = sg.next(n)) {
-      wait_warp(&bar[kBarRawFull + raw.slot], raw.phase, sh, p.a.status);
+      wait(bar, kBarRawFull + raw.slot, raw.phase);
+      __syncwarp();
       const uint32_t base = raw0 + raw.slot * kRawBytes;
       uint4 w0, w1;
       uint32_t sc;
       auto load = [&](int ch) {
-        const uint32_t half = base + code_off + (ch >> 2) * (kPageTokens * 128);
-        w0 = ld_shared_v4(half + (((2 * (ch & 3)) ^ (row & 7)) << 4));
-        w1 = ld_shared_v4(half + (((2 * (ch & 3) + 1) ^ (row & 7)) << 4));
+        const uint32_t at = (base + code_off + (ch >> 2) * kHalfBytes) ^ ((ch & 3) << 5);
+        w0 = ld_shared_v4(at);
+        w1 = ld_shared_v4(at ^ 16);
         sc = ld_shared_u32(base + kRawCodeBytes + row * kScaleBytes + 4 * ch);
       };
       load(0);
@@ -411,13 +449,11 @@ __device__ void unpack_rows_role(const AttendPackedParams &p, const Shared &sh, 
 #pragma unroll
           for (int k = 0; k < 4; ++k) r[4 * i + k] = mul_f16x2(v[k], s);
         }
+        tmem_st32(t_dst + out.acquire() * 32, r);
         out.hand_over(lane);
-        tmem_st32(t_dst + out.acquire(sh, p.a.status) * 32, r);
-        out.stored();
       }
-      if (lane == 0) mbar_arrive(&bar[kBarRawEmpty + raw.slot]);
+      if (lane == 0) arrive(bar[kBarRawEmpty + raw.slot]);
       raw.step(kRawSlots);
-      out.hand_over(lane);
     }
   }
 }
@@ -435,35 +471,36 @@ __device__ __forceinline__ int k_of_row(int r) {  // K index of tile row r
 
 __device__ void unpack_latents_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, long long t0,
                                     long long t1, int wq, int lane) {
-  uint64_t *bar = sh.bar;
+  const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.a.status};
   const int g = lane >> 2, c = lane & 3;
   const int group = 8 * wq + g;
   // the group's eight bytes in a row: half, 16-byte unit, which eight of it; the thread's rows of
   // a chunk are 2c + b + 8h, whose unit is the same for both h
   const uint32_t unit = 4 * (wq & 1) + (g >> 1);
-  const uint32_t off0 = (wq >> 1) * (kPageTokens * 128) + (g & 1) * 8 + (2 * c) * 128;
+  const uint32_t off0 = (wq >> 1) * kHalfBytes + (g & 1) * 8 + (2 * c) * 128;
   const uint32_t row_off[2] = {off0 + ((unit ^ (2 * c)) << 4), off0 + 128 + ((unit ^ (2 * c + 1)) << 4)};
   const uint32_t scale_off = kRawCodeBytes + (2 * c) * kScaleBytes + group;
   const uint32_t raw0 = smem_u32(sh.base);
   const uint32_t t_dst = tmem + ((uint32_t)(wq * 32) << 16) + kTmemVA;
   Ring raw;
-  Stager out{&bar[kBarVAFull], &bar[kBarVAEmpty], Ring(), Stager::kNone};
+  Stager out{bar, kBarVAFull, kBarVAEmpty, Ring()};
   SegIter it(t0, t1, iq);
   Segment sg;
   while (it.next(p, sg)) {
     for (int n = sg.first(); n < sg.hi; n = sg.next(n)) {
-      wait_warp(&bar[kBarRawFull + raw.slot], raw.phase, sh, p.a.status);
+      wait(bar, kBarRawFull + raw.slot, raw.phase);
+      __syncwarp();
       const uint32_t base = raw0 + raw.slot * kRawBytes;
       const int j0 = sg.q.seq.tile(n) * kTile;
       const bool whole = sg.q.every_row(j0, kTile);
       uint2 w[4];
       uint32_t s[4];
       auto load = [&](int ks) {
-        const uint32_t page = base + (ks >> 2) * kPageCodeBytes + (ks & 3) * (16 * 128);
+        const uint32_t rows = base + ks * (16 * 128);
         const uint32_t sp = base + scale_off + ks * 16 * kScaleBytes;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {  // row 2c + k % 2 + 8 (k / 2)
-          w[k] = ld_shared_v2(page + row_off[k & 1] + (k >> 1) * (8 * 128));
+          w[k] = ld_shared_v2(rows + row_off[k & 1] + (k >> 1) * (8 * 128));
           s[k] = ld_shared_u8(sp + ((k & 1) + 8 * (k >> 1)) * kScaleBytes);
         }
       };
@@ -500,15 +537,13 @@ __device__ void unpack_latents_role(const AttendPackedParams &p, const Shared &s
             }
           }
         }
-        out.hand_over(lane);
-        const uint32_t dst = t_dst + out.acquire(sh, p.a.status) * 32;
+        const uint32_t dst = t_dst + out.acquire() * 32;
         tmem_st16x256_x4(dst, r[0]);
         tmem_st16x256_x4(dst + (16u << 16), r[1]);
-        out.stored();
+        out.hand_over(lane);
       }
-      if (lane == 0) mbar_arrive(&bar[kBarRawEmpty + raw.slot]);
+      if (lane == 0) arrive(bar[kBarRawEmpty + raw.slot]);
       raw.step(kRawSlots);
-      out.hand_over(lane);
     }
   }
 }
@@ -576,7 +611,7 @@ __device__ __forceinline__ float sum_columns(float (&v)[32], int lane) {
 
 __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int grp, int iq,
                              long long t0, long long t1, int warp, int lane) {
-  uint64_t *bar = sh.bar;
+  const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.a.status};
   const int w = warp - 3, wg = w >> 2, wq = warp & 3;
   const int tid = wq * 32 + lane;    // within the warpgroup
   const int row = wq * 32 + lane;    // tile row = tensor-memory lane
@@ -611,8 +646,7 @@ __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint
     for (; n < sg.hi; n = sg.next(n), ++tiles) {
       const uint32_t pb = tiles & 1;
       const int j0 = sg.q.seq.tile(n) * kTile;
-      const bool vis = sg.q.row(j0 + row);
-      mbar_wait(&bar[kBarSFull], tiles & 1, sh.abort_flag, p.a.status);
+      wait(bar, kBarSFull, tiles & 1);
       __syncwarp();
       tc_fence_after();
       float x[32];  // score - m, in log2 units
@@ -622,23 +656,23 @@ __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[kBarSEmpty]);
+        if (lane == 0) arrive(bar[kBarSEmpty]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float4 c4 = cs4[j], mm = m4[j];
-          x[4 * j + 0] = fmaf(__uint_as_float(s[4 * j + 0]), c4.x, -mm.x);
-          x[4 * j + 1] = fmaf(__uint_as_float(s[4 * j + 1]), c4.y, -mm.y);
-          x[4 * j + 2] = fmaf(__uint_as_float(s[4 * j + 2]), c4.z, -mm.z);
-          x[4 * j + 3] = fmaf(__uint_as_float(s[4 * j + 3]), c4.w, -mm.w);
+          fma_f32x2(x[4 * j], x[4 * j + 1], __uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1]), c4.x, c4.y, mm.x, mm.y);
+          fma_f32x2(x[4 * j + 2], x[4 * j + 3], __uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3]), c4.z, c4.w,
+                    mm.z, mm.w);
         }
       }
-      if (!vis) {
+      if (!sg.q.every_row(j0, kTile)) {
+        const bool vis = sg.q.row(j0 + row);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = -INFINITY;
+        for (int j = 0; j < 32; ++j) x[j] = vis ? x[j] : -INFINITY;
       }
-      float top = x[0];
+      float top = fmaxf(x[0], x[1]);
 #pragma unroll
-      for (int j = 1; j < 32; ++j) top = fmaxf(top, x[j]);
+      for (int j = 2; j < 32; j += 2) top = fmaxf(fmaxf(top, x[j]), x[j + 1]);  // three-operand maxima
       const bool raise = named_bar_or(bar_id, 128, first || top > kTau + kShift);
       if (raise) {
         int mine = 0;
@@ -657,7 +691,7 @@ __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint
           if (mt == -INFINITY || (!first && d < 0.f)) d = 0.f;
           sh.rise[h] = d;
           sh.alpha[h] = exp2_approx(-d);
-          sh.m[h] += d;
+          sh.m[h] -= d;
         }
         named_bar_sync(bar_id, 128);
 #pragma unroll
@@ -670,15 +704,14 @@ __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const float p0 = exp2_approx(x[2 * j]), p1 = exp2_approx(x[2 * j + 1]);
-        l_part[2 * j] += p0;
-        l_part[2 * j + 1] += p1;
+        add_f32x2(l_part[2 * j], l_part[2 * j + 1], p0, p1);
         pw[j] = pack_f16x2(p0, p1);
       }
       // this P buffer is free (the value MMAs of two tiles ago are done)
-      mbar_wait(&bar[kBarPEmpty + pb], ((tiles >> 1) & 1) ^ 1, sh.abort_flag, p.a.status);
+      wait(bar, kBarPEmpty + pb, ((tiles >> 1) & 1) ^ 1);
       if (raise && !first) {
         // the running max moved: once the last tile's value MMAs are done, rescale O^T
-        mbar_wait(&bar[kBarPEmpty + (pb ^ 1)], ((tiles - 1) >> 1) & 1, sh.abort_flag, p.a.status);
+        wait(bar, kBarPEmpty + (pb ^ 1), ((tiles - 1) >> 1) & 1);
         __syncwarp();
         tc_fence_after();
 #pragma unroll 1
@@ -700,7 +733,7 @@ __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[kBarPFull + pb]);
+      if (lane == 0) arrive(bar[kBarPFull + pb]);
       first = false;
     }
     // ---- epilogue: the partial (O, m, l)
@@ -708,10 +741,10 @@ __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint
     named_bar_sync(bar_id, 128);
     if (tid < 32) {
       const int h = col0 + tid;
-      p.a.part_m[slot * kHeads + h] = sh.m[h];
+      p.a.part_m[slot * kHeads + h] = -sh.m[h];
       p.a.part_l[slot * kHeads + h] = sh.red[h] + sh.red[kHeads + h] + sh.red[2 * kHeads + h] + sh.red[3 * kHeads + h];
     }
-    mbar_wait(&bar[kBarOFull], segs & 1, sh.abort_flag, p.a.status);
+    wait(bar, kBarOFull, segs & 1);
     __syncwarp();
     tc_fence_after();
     float *po = p.a.part_o + slot * kHeads * kLatent;
@@ -725,7 +758,7 @@ __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bar[kBarOEmpty]);
+    if (lane == 0) arrive(bar[kBarOEmpty]);
     ++segs;
   }
 }
@@ -796,12 +829,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     score_mma_role(p, sh, tmem, iq, t0, t1);
   } else if (warp == 2) {
     value_mma_role(p, sh, tmem, iq, t0, t1);
-  } else if (warp >= 15) {
-    unpack_latents_role(p, sh, tmem, iq, t0, t1, warp & 3, lane);
-  } else if (warp >= 11) {
+  } else if (warp < 11) {
+    softmax_role(p, sh, tmem, g, iq, t0, t1, warp, lane);
+  } else if (warp < 15) {
     unpack_rows_role(p, sh, tmem, iq, t0, t1, warp & 3, lane);
   } else {
-    softmax_role(p, sh, tmem, g, iq, t0, t1, warp, lane);
+    unpack_latents_role(p, sh, tmem, iq, t0, t1, warp & 3, lane);
   }
 
   __syncwarp();
