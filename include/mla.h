@@ -56,6 +56,7 @@ typedef int32_t mla_status;
 #define MLA_ERR_WORKSPACE 4    /* workspace pointer null or ws_bytes too small */
 #define MLA_ERR_INDEX 5        /* device: page id / cache index / length out of range */
 #define MLA_ERR_TIMEOUT 6      /* device: a bounded pipeline wait expired */
+#define MLA_ERR_PAGES 7        /* device: a page operation found no free page */
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *mla_status_string(mla_status s);
@@ -287,6 +288,48 @@ mla_status mla_attend_packed(const uint16_t *q_tilde, const uint8_t *pool, const
                              const int32_t *seq_lens, int B, int Q, int H, int R, int page_size, int max_pages,
                              int num_pages, float unit, int window, int sinks, float scale, void *workspace,
                              size_t ws_bytes, uint16_t *o_latent, float *lse, int32_t *status, void *stream);
+
+/*
+ * Page bookkeeping of a paged cache (bf16 or 4-bit rows), the part that mla_cache_* leave to the
+ * caller: which pages of the pool a sequence's positions map to.
+ *   pool       num_pages pages of page_bytes each (65,536 for bf16 rows, 18,432 for 4-bit ones)
+ *   page_table [B, max_pages] int32, -1 = unmapped        seq_lens [B] int32
+ *   refs       [num_pages] int32, the number of table entries that map the page; 0 = free
+ * The calls keep refs in step with page_table, and expect it so.  Free pages are taken lowest first, by
+ * sequence (fork: by list entry) and then by position; the results do not depend on timing.
+ * workspace: mla_pages_workspace_bytes(n, num_pages), n = B (reserve), n forks, 1 (compact); it
+ * holds nothing between calls.  The pages describe no allocator.
+ *
+ * mla_pages_reserve: gives every sequence room for Q more rows (before mla_cache_append_*): maps its
+ *   unmapped pages among those of positions L_b .. L_b + Q - 1, and replaces a page among them that
+ *   other entries map too (refs > 1 at the call) by a copy of its own.
+ * mla_pages_fork: sequence children[k] becomes a copy of sequence parents[k]: full pages are shared,
+ *   the partial last page is copied to a fresh one, the length is set.  A child must be empty (all
+ *   entries -1), occur once in children and not in parents.  Rows that were there before a fork
+ *   are shared: make room by mla_pages_reserve before rewriting any of them (an append after a
+ *   fork needs no more than usual; mla_cache_truncate_* beyond the fork point would write them).
+ * mla_pages_release: unmaps the entries at and behind ceil(L_b / 64): after a truncation, or, with
+ *   seq_lens[b] = 0, all of a sequence.
+ * mla_pages_compact: moves the pages that are used (refs > 0) and lie at or above n_used, their
+ *   number, to the free pages below it, in order; refs and all B tables follow.  n_used: device int32.
+ *   Afterwards pages n_used .. num_pages - 1 are free.
+ * A sequence or list entry whose positions, pages or indexes are out of range (or, fork: as above) is
+ * left untouched and sets MLA_ERR_INDEX; one whose pages are no longer free, and every later one
+ * that needs a page, is left untouched and sets MLA_ERR_PAGES; the others proceed.  Pages keep
+ * their content when they become free.
+ */
+size_t mla_pages_workspace_bytes(int n, int num_pages);
+mla_status mla_pages_reserve(void *pool, int page_bytes, int32_t *page_table, const int32_t *seq_lens, int32_t *refs,
+                             int B, int Q, int max_pages, int num_pages, void *workspace, size_t ws_bytes,
+                             int32_t *status, void *stream);
+mla_status mla_pages_fork(void *pool, int page_bytes, int32_t *page_table, int32_t *seq_lens, int32_t *refs,
+                          const int32_t *parents, const int32_t *children, int n, int B, int max_pages, int num_pages,
+                          void *workspace, size_t ws_bytes, int32_t *status, void *stream);
+mla_status mla_pages_release(int32_t *page_table, const int32_t *seq_lens, int32_t *refs, int B, int max_pages,
+                             int num_pages, int32_t *status, void *stream);
+mla_status mla_pages_compact(void *pool, int page_bytes, int32_t *page_table, int32_t *refs, int B, int max_pages,
+                             int num_pages, int32_t *n_used, void *workspace, size_t ws_bytes, int32_t *status,
+                             void *stream);
 
 /*
  * k-pool index producer for mla_attend_indexed.  Page "GLM-5.3-Flash engine (c/glm53.c)"

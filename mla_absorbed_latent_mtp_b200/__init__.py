@@ -15,6 +15,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmla_b200.so")
 
 MLA_OK, MLA_ERR_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA, MLA_ERR_WORKSPACE, MLA_ERR_INDEX, MLA_ERR_TIMEOUT = range(7)
+MLA_ERR_PAGES = 7
 MODE_DENSE, MODE_PAGED, MODE_INDEXED = 0, 1, 2
 H, D, R, PAGE = 64, 256, 512, 64
 PACKED_ROW = R // 2 + R // 16  # bytes of a row of the 4-bit cache
@@ -25,7 +26,8 @@ EXPORTS = ("mla_status_string", "mla_last_error_string", "mla_absorb_q", "mla_at
            "mla_cache_append_dense", "mla_cache_append_paged", "mla_cache_truncate_dense", "mla_cache_truncate_paged",
            "mla_debug_wait_timeout", "mla_kpool_keys", "mla_kpool_select", "mla_attend_up_dense",
            "mla_attend_up_paged", "mla_attend_up_indexed", "mla_expand_kv", "mla_prefill_expanded",
-           "mla_cache_append_packed", "mla_cache_truncate_packed", "mla_cache_unpack", "mla_attend_packed")
+           "mla_cache_append_packed", "mla_cache_truncate_packed", "mla_cache_unpack", "mla_attend_packed",
+           "mla_pages_workspace_bytes", "mla_pages_reserve", "mla_pages_fork", "mla_pages_release", "mla_pages_compact")
 
 
 class MLAError(RuntimeError):
@@ -82,7 +84,14 @@ def lib():
     L.mla_cache_unpack.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, vp]
     L.mla_attend_packed.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, f32, i32, i32, f32, vp, sz, vp,
                                     vp, vp, vp]
-    for name in ("mla_cache_append_packed", "mla_cache_truncate_packed", "mla_cache_unpack", "mla_attend_packed"):
+    L.mla_pages_workspace_bytes.argtypes = [i32, i32]
+    L.mla_pages_workspace_bytes.restype = sz
+    L.mla_pages_reserve.argtypes = [vp, i32, vp, vp, vp, i32, i32, i32, i32, vp, sz, vp, vp]
+    L.mla_pages_fork.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, sz, vp, vp]
+    L.mla_pages_release.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp]
+    L.mla_pages_compact.argtypes = [vp, i32, vp, vp, i32, i32, i32, vp, vp, sz, vp, vp]
+    for name in ("mla_cache_append_packed", "mla_cache_truncate_packed", "mla_cache_unpack", "mla_attend_packed",
+                 "mla_pages_reserve", "mla_pages_fork", "mla_pages_release", "mla_pages_compact"):
         getattr(L, name).restype = ctypes.c_int32
     for name in ("mla_absorb_q", "mla_up_proj", "mla_attend_dense", "mla_attend_paged", "mla_attend_indexed",
                  "mla_debug_gather", "mla_attend_dense_noalloc", "mla_cache_append_dense", "mla_cache_append_paged",
@@ -534,6 +543,87 @@ def mla_attend_packed(q_tilde, pool, page_table, seq_lens, unit=1.0, window=0, s
         pool.shape[0], unit, window, sinks, scale, _ptr(workspace), workspace.numel() * workspace.element_size(),
         _ptr(o_latent), _ptr(lse), _ptr(status), _stream(stream)))
     return o_latent, lse
+
+
+def mla_pages_workspace_bytes(n: int, num_pages: int) -> int:
+    return int(lib().mla_pages_workspace_bytes(n, num_pages))
+
+
+def new_pages_workspace(n: int, num_pages: int):
+    """Allocate (with torch) the workspace the page calls need for n sequences or forks."""
+    import torch
+    return torch.empty(max(mla_pages_workspace_bytes(n, num_pages), 16), dtype=torch.uint8, device="cuda")
+
+
+def _check_pages(page_table, refs, status, seq_lens=None, lens_required=True):
+    _require(page_table, "page_table", "i32", (None, None))
+    _require(refs, "refs", "i32", (None,))
+    _require(seq_lens, "seq_lens", "i32", min_numel=page_table.shape[0], optional=not lens_required)
+    _require(status, "status", "i32", min_numel=1, optional=True)
+
+
+def _check_page_pool(pool, refs, n, workspace):
+    """pool [P, 64, ...] of any dtype, contiguous; returns (bytes per page, workspace)."""
+    if pool is None or not pool.is_contiguous() or pool.dim() < 2 or pool.shape[1] != PAGE:
+        raise ValueError(f"pool must be a contiguous [P, {PAGE}, ...] tensor")
+    P = int(pool.shape[0])
+    if refs.numel() != P:
+        raise ValueError(f"refs must have one element per page ({P}), got {refs.numel()}")
+    if workspace is not None:
+        _require(workspace, "workspace", "u8", min_numel=mla_pages_workspace_bytes(n, P))
+    return pool.numel() * pool.element_size() // max(P, 1)
+
+
+def mla_pages_reserve(pool, page_table, seq_lens, refs, q_len, workspace=None, status=None, stream=None):
+    """Map pages for the next q_len rows of every sequence; shared pages among them become own copies."""
+    _check_pages(page_table, refs, status, seq_lens)
+    B, max_pages = page_table.shape
+    page_bytes = _check_page_pool(pool, refs, B, workspace)
+    _check_cuda(pool, page_table, seq_lens, refs, workspace, status)
+    workspace = new_pages_workspace(B, pool.shape[0]) if workspace is None else workspace
+    _check("mla_pages_reserve", lib().mla_pages_reserve(
+        _ptr(pool), page_bytes, _ptr(page_table), _ptr(seq_lens), _ptr(refs), B, q_len, max_pages, pool.shape[0],
+        _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
+
+
+def mla_pages_fork(pool, page_table, seq_lens, refs, parents, children, workspace=None, status=None, stream=None):
+    """Sequence children[k] (empty) becomes a copy of sequence parents[k] that shares its full pages."""
+    _check_pages(page_table, refs, status, seq_lens)
+    _require(parents, "parents", "i32", (None,))
+    n = parents.shape[0]
+    _require(children, "children", "i32", (n,))
+    B, max_pages = page_table.shape
+    page_bytes = _check_page_pool(pool, refs, n, workspace)
+    _check_cuda(pool, page_table, seq_lens, refs, parents, children, workspace, status)
+    workspace = new_pages_workspace(n, pool.shape[0]) if workspace is None else workspace
+    _check("mla_pages_fork", lib().mla_pages_fork(
+        _ptr(pool), page_bytes, _ptr(page_table), _ptr(seq_lens), _ptr(refs), _ptr(parents), _ptr(children), n, B,
+        max_pages, pool.shape[0], _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
+
+
+def mla_pages_release(page_table, seq_lens, refs, status=None, stream=None):
+    """Unmap the entries behind each sequence's last row (all of them where its length is 0)."""
+    _check_pages(page_table, refs, status, seq_lens)
+    _check_cuda(page_table, seq_lens, refs, status)
+    _check("mla_pages_release", lib().mla_pages_release(
+        _ptr(page_table), _ptr(seq_lens), _ptr(refs), page_table.shape[0], page_table.shape[1], refs.numel(),
+        _ptr(status), _stream(stream)))
+
+
+def mla_pages_compact(pool, page_table, refs, n_used=None, workspace=None, status=None, stream=None):
+    """Move the used pages to the front of the pool; returns n_used [1] int32, their number."""
+    import torch
+    _check_pages(page_table, refs, status, lens_required=False)
+    _require(n_used, "n_used", "i32", min_numel=1, optional=True)
+    page_bytes = _check_page_pool(pool, refs, 1, workspace)
+    _check_cuda(pool, page_table, refs, n_used, workspace, status)
+    if n_used is None:
+        n_used = torch.empty(1, dtype=torch.int32, device=pool.device)
+    workspace = new_pages_workspace(1, pool.shape[0]) if workspace is None else workspace
+    _check("mla_pages_compact", lib().mla_pages_compact(
+        _ptr(pool), page_bytes, _ptr(page_table), _ptr(refs), page_table.shape[0], page_table.shape[1], pool.shape[0],
+        _ptr(n_used), _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
+    return n_used
 
 
 def mla_debug_wait_timeout(limit_cycles, status, stream=None):

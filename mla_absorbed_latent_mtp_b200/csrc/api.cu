@@ -367,6 +367,8 @@ const char *mla_status_string(mla_status s) {
       return "MLA_ERR_INDEX";
     case MLA_ERR_TIMEOUT:
       return "MLA_ERR_TIMEOUT";
+    case MLA_ERR_PAGES:
+      return "MLA_ERR_PAGES";
     default:
       return "MLA_ERR_UNKNOWN";
   }

@@ -410,3 +410,125 @@ def packed_values(packed: np.ndarray, unit: float = 1.0) -> np.ndarray:
     v = np.where(code & 8, -1.0, 1.0) * E2M1_VALUES[code & 7]
     s = np.repeat(e4m3_value(packed[..., 256:]), PACKED_GROUP, axis=-1)
     return v * s * unit
+
+
+# ----------------------------------------------------------------------------- page bookkeeping
+class PageBook:
+    """The paged cache's bookkeeping, one entry at a time: table [B, max_pages] (-1 unmapped), lens [B],
+    refs [P] and a pool [P, ...].  Each call returns "ok", "index" or "pages" (the first error)."""
+
+    def __init__(self, table, lens, refs, pool, page=64):
+        self.table, self.lens, self.refs, self.pool, self.page = table, lens, refs, pool, page
+
+    def _free(self):
+        return [int(p) for p in np.flatnonzero(self.refs == 0)]
+
+    def _run(self, entries):
+        """entries: per list entry None (refused) or a list of (row, position, source page or None)
+        to map; applied in order to the pages that are free now."""
+        free, at, full, status = self._free(), 0, False, "ok"
+        done = []
+        for e in entries:
+            if e is None:
+                status = status if status != "ok" else "index"
+                done.append(False)
+                continue
+            if e and (full or at + len(e) > len(free)):
+                full = True
+                status = status if status != "ok" else "pages"
+                done.append(False)
+                continue
+            done.append(True)
+            for row, k, src in e:
+                p = free[at]
+                at += 1
+                if src is not None:
+                    self.pool[p] = self.pool[src]
+                self.table[row, k] = p
+                self.refs[p] = 1
+        return status, done
+
+    def reserve(self, q_len):
+        B, max_pages = self.table.shape
+        refs0 = self.refs.copy()
+        entries, drops = [], []
+        for b in range(B):
+            L = int(self.lens[b])
+            if L < 0 or L + q_len > max_pages * self.page:
+                entries.append(None)
+                drops.append([])
+                continue
+            need, drop, ok = [], [], True
+            for k in range(L // self.page, (L + q_len - 1) // self.page + 1):
+                p = int(self.table[b, k])
+                ok = ok and -1 <= p < len(self.refs)
+                if ok and (p < 0 or refs0[p] > 1):
+                    need.append((b, k, p if p >= 0 else None))
+                    drop += [p] if p >= 0 else []
+            entries.append(need if ok else None)
+            drops.append(drop)
+        status, done = self._run(entries)
+        for ok, drop in zip(done, drops):
+            if ok:
+                for p in drop:
+                    self.refs[p] -= 1
+        return status
+
+    def fork(self, parents, children):
+        B, max_pages = self.table.shape
+        before, lens0 = self.table.copy(), self.lens.copy()
+        entries = []
+        for k, (par, child) in enumerate(zip(parents, children)):
+            ok = 0 <= par < B and 0 <= child < B and par != child
+            ok = ok and list(children).count(child) == 1 and child not in list(parents)
+            ok = ok and bool((before[child] == -1).all()) and 0 <= lens0[par] <= max_pages * self.page
+            if ok:
+                used = before[par, : -(-int(lens0[par]) // self.page)]
+                ok = bool(((used >= 0) & (used < len(self.refs))).all())
+            if not ok:
+                entries.append(None)
+                continue
+            L = int(lens0[par])
+            entries.append([(child, L // self.page, int(before[par, L // self.page]))] if L % self.page else [])
+        status, done = self._run(entries)
+        for (par, child), ok in zip(zip(parents, children), done):
+            if ok:
+                full = int(lens0[par]) // self.page
+                self.table[child, :full] = before[par, :full]
+                for p in before[par, :full]:
+                    self.refs[p] += 1
+                self.lens[child] = lens0[par]
+        return status
+
+    def release(self):
+        B, max_pages = self.table.shape
+        status = "ok"
+        for b in range(B):
+            L = int(self.lens[b])
+            if L < 0 or L > max_pages * self.page:
+                status = "index"
+                continue
+            for k in range(-(-L // self.page), max_pages):
+                p = int(self.table[b, k])
+                if p == -1:
+                    continue
+                if p < 0 or p >= len(self.refs):
+                    status = "index"
+                    continue
+                self.refs[p] -= 1
+                self.table[b, k] = -1
+        return status
+
+    def compact(self):
+        used = np.flatnonzero(self.refs > 0)
+        n = len(used)
+        src = [int(p) for p in used if p >= n]
+        dst = [int(p) for p in np.flatnonzero(self.refs == 0) if p < n]
+        to = dict(zip(src, dst))
+        for s, d in to.items():
+            self.pool[d] = self.pool[s]
+            self.refs[d], self.refs[s] = self.refs[s], 0
+        for idx, p in np.ndenumerate(self.table):
+            if int(p) in to:
+                self.table[idx] = to[int(p)]
+        return n
