@@ -133,6 +133,23 @@ mla_status mla_attend_indexed(const uint16_t *q_tilde, const uint16_t *cache, co
                               float *lse, int32_t *status, void *stream);
 
 /*
+ * mla_attend_dense / mla_attend_paged with a sliding window and sinks: the query at position t sees the
+ * rows j <= t with t - j < window (its own row and the window - 1 before it) or j < sinks (the first
+ * rows of the sequence, which stay visible).  window >= 1, sinks >= 0; everything else as there.
+ * Only tiles with a visible row are read: paged, a page outside every query's window and the sinks
+ * need not be mapped.  Rows that a query does not see may hold any bits.  lse sums the unrounded
+ * weights (mla_attend_dense sums them as rounded to bf16), so the two agree to rounding where the
+ * window covers the sequence.  Lmax, max_pages * 64 < 2^31 - 64.  The pages describe no window.
+ */
+mla_status mla_attend_window_dense(const uint16_t *q_tilde, const uint16_t *cache, const int32_t *seq_lens, int B, int Q,
+                                   int H, int R, int Lmax, float scale, int window, int sinks, void *workspace,
+                                   size_t ws_bytes, uint16_t *o_latent, float *lse, int32_t *status, void *stream);
+mla_status mla_attend_window_paged(const uint16_t *q_tilde, const uint16_t *pool, const int32_t *page_table,
+                                   const int32_t *seq_lens, int B, int Q, int H, int R, int page_size, int max_pages,
+                                   int num_pages, float scale, int window, int sinks, void *workspace, size_t ws_bytes,
+                                   uint16_t *o_latent, float *lse, int32_t *status, void *stream);
+
+/*
  * Value up-projection, Module 05 section 3:  out[n,h,:] = U_h^V o_latent[n,h,:].
  *   o_latent [n, H, R] bf16, w_uv [H, D, R] bf16 (v = U_h^V c), out [n, H, D] bf16.
  */

@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(_HERE, "libmla_b200.so")
 
 MLA_OK, MLA_ERR_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA, MLA_ERR_WORKSPACE, MLA_ERR_INDEX, MLA_ERR_TIMEOUT = range(7)
 MLA_ERR_PAGES = 7
-MODE_DENSE, MODE_PAGED, MODE_INDEXED = 0, 1, 2
+MODE_DENSE, MODE_PAGED, MODE_INDEXED, MODE_PACKED = 0, 1, 2, 3
 H, D, R, PAGE = 64, 256, 512, 64
 PACKED_ROW = R // 2 + R // 16  # bytes of a row of the 4-bit cache
 SCALE = 1.0 / 16.0
@@ -26,6 +26,7 @@ EXPORTS = ("mla_status_string", "mla_last_error_string", "mla_absorb_q", "mla_at
            "mla_cache_append_dense", "mla_cache_append_paged", "mla_cache_truncate_dense", "mla_cache_truncate_paged",
            "mla_debug_wait_timeout", "mla_kpool_keys", "mla_kpool_select", "mla_attend_up_dense",
            "mla_attend_up_paged", "mla_attend_up_indexed", "mla_expand_kv", "mla_prefill_expanded",
+           "mla_attend_window_dense", "mla_attend_window_paged",
            "mla_cache_append_packed", "mla_cache_truncate_packed", "mla_cache_unpack", "mla_attend_packed",
            "mla_pages_workspace_bytes", "mla_pages_reserve", "mla_pages_fork", "mla_pages_release", "mla_pages_compact")
 
@@ -90,7 +91,10 @@ def lib():
     L.mla_pages_fork.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, sz, vp, vp]
     L.mla_pages_release.argtypes = [vp, vp, vp, i32, i32, i32, vp, vp]
     L.mla_pages_compact.argtypes = [vp, i32, vp, vp, i32, i32, i32, vp, vp, sz, vp, vp]
-    for name in ("mla_cache_append_packed", "mla_cache_truncate_packed", "mla_cache_unpack", "mla_attend_packed",
+    L.mla_attend_window_dense.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, f32, i32, i32, vp, sz, vp, vp, vp, vp]
+    L.mla_attend_window_paged.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, f32, i32, i32, vp, sz, vp,
+                                          vp, vp, vp]
+    for name in ("mla_attend_window_dense", "mla_attend_window_paged", "mla_cache_append_packed", "mla_cache_truncate_packed", "mla_cache_unpack", "mla_attend_packed",
                  "mla_pages_reserve", "mla_pages_fork", "mla_pages_release", "mla_pages_compact"):
         getattr(L, name).restype = ctypes.c_int32
     for name in ("mla_absorb_q", "mla_up_proj", "mla_attend_dense", "mla_attend_paged", "mla_attend_indexed",
@@ -291,6 +295,40 @@ def mla_attend_indexed(q_tilde, cache, indices, seq_lens=None, scale=SCALE, work
         _ptr(q_tilde), _ptr(cache), _ptr(indices), _ptr(seq_lens), B, Q, H, R, cache.shape[1], indices.shape[2],
         scale, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(o_latent), _ptr(lse),
         _ptr(status), _stream(stream)))
+    return o_latent, lse
+
+
+def mla_attend_window_dense(q_tilde, cache, window, sinks=0, seq_lens=None, scale=SCALE, workspace=None, o_latent=None,
+                            lse=None, status=None, want_lse=True, stream=None):
+    """mla_attend_dense where each query sees its last `window` rows and the first `sinks` ones."""
+    B, Q = _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens)
+    _require(cache, "cache", "bf16", (None, None, R))
+    if cache.shape[0] < B:
+        raise ValueError(f"cache holds {cache.shape[0]} sequences, q_tilde {B}")
+    _check_cuda(q_tilde, cache, seq_lens, workspace, o_latent, lse, status)
+    workspace = new_workspace(B, Q) if workspace is None else workspace
+    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
+    _check("mla_attend_window_dense", lib().mla_attend_window_dense(
+        _ptr(q_tilde), _ptr(cache), _ptr(seq_lens), B, Q, H, R, cache.shape[1], scale, window, sinks, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(o_latent), _ptr(lse), _ptr(status), _stream(stream)))
+    return o_latent, lse
+
+
+def mla_attend_window_paged(q_tilde, pool, page_table, seq_lens, window, sinks=0, scale=SCALE, workspace=None,
+                            o_latent=None, lse=None, status=None, want_lse=True, stream=None):
+    """Paged counterpart of mla_attend_window_dense (pool [P, 64, R], page_table [B, max_pages])."""
+    B, Q = _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens, seq_lens_required=True)
+    _require(pool, "pool", "bf16", (None, PAGE, R))
+    _require(page_table, "page_table", "i32", (None, None))
+    if page_table.shape[0] < B:
+        raise ValueError(f"page_table has {page_table.shape[0]} rows, q_tilde {B} sequences")
+    _check_cuda(q_tilde, pool, page_table, seq_lens, workspace, o_latent, lse, status)
+    workspace = new_workspace(B, Q) if workspace is None else workspace
+    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
+    _check("mla_attend_window_paged", lib().mla_attend_window_paged(
+        _ptr(q_tilde), _ptr(pool), _ptr(page_table), _ptr(seq_lens), B, Q, H, R, pool.shape[1], page_table.shape[1],
+        pool.shape[0], scale, window, sinks, _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(o_latent), _ptr(lse), _ptr(status), _stream(stream)))
     return o_latent, lse
 
 
@@ -672,11 +710,17 @@ def mla_kpool_select(pooled, w_query, pool, topk, seq_lens=None, with_tail=True,
 
 
 def mla_decode(q, w_uk, w_uv, cache, seq_lens=None, *, mode=MODE_DENSE, page_table=None, indices=None,
-               scale=SCALE, workspace=None, status=None, stream=None, fused=False):
-    """The whole path: absorb -> attend (dense / paged / indexed) -> up-project.  With
-    fused=True the up-projection runs inside the split-L merge (mla_attend_up_*).
+               scale=SCALE, workspace=None, status=None, stream=None, fused=False, window=0, sinks=0, unit=1.0):
+    """The whole path: absorb -> attend (dense / paged / indexed / packed) -> up-project.  With
+    fused=True the up-projection runs inside the split-L merge (mla_attend_up_*).  window > 0 (not
+    for index lists): each query sees its last `window` rows and the first `sinks` ones.  unit: of a
+    packed (4-bit) cache.
 
     q [B, Q, H, D] bf16 -> out [B, Q, H, D] bf16 (and lse [B, Q, H])."""
+    if fused and (window or mode == MODE_PACKED):
+        raise ValueError("fused=True has no windowed or packed form")
+    if window and mode == MODE_INDEXED:
+        raise ValueError("index lists take no window")
     qt = mla_absorb_q(q, w_uk, stream=stream)
     if fused:
         if mode == MODE_DENSE:
@@ -686,7 +730,16 @@ def mla_decode(q, w_uk, w_uv, cache, seq_lens=None, *, mode=MODE_DENSE, page_tab
                                        stream=stream)
         return mla_attend_up_indexed(qt, cache, indices, w_uv, seq_lens, scale, workspace, status=status,
                                      stream=stream)
-    if mode == MODE_DENSE:
+    if mode == MODE_PACKED:
+        o, lse = mla_attend_packed(qt, cache, page_table, seq_lens, unit, window, sinks, scale, workspace,
+                                   status=status, stream=stream)
+    elif mode == MODE_DENSE and window:
+        o, lse = mla_attend_window_dense(qt, cache, window, sinks, seq_lens, scale, workspace, status=status,
+                                         stream=stream)
+    elif mode == MODE_PAGED and window:
+        o, lse = mla_attend_window_paged(qt, cache, page_table, seq_lens, window, sinks, scale, workspace,
+                                         status=status, stream=stream)
+    elif mode == MODE_DENSE:
         o, lse = mla_attend_dense(qt, cache, seq_lens, scale, workspace, status=status, stream=stream)
     elif mode == MODE_PAGED:
         o, lse = mla_attend_paged(qt, cache, page_table, seq_lens, scale, workspace, status=status, stream=stream)

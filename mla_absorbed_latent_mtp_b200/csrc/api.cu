@@ -104,7 +104,8 @@ static mla_status attend_common(int mode, const uint16_t *q_tilde, const uint16_
                                 const int32_t *indices, const int32_t *seq_lens, int B, int Q, int H, int R, int Lmax,
                                 int page_size, int max_pages, int num_pages, int K, float scale, void *workspace,
                                 size_t ws_bytes, uint16_t *o_latent, float *lse, int32_t *status, void *stream,
-                                const uint16_t *w_uv = nullptr, int D = 0, uint16_t *out = nullptr) {
+                                const uint16_t *w_uv = nullptr, int D = 0, uint16_t *out = nullptr, int window = 0,
+                                int sinks = 0) {
   const bool fused = (w_uv != nullptr || out != nullptr);
   if (q_tilde == nullptr || cache == nullptr) return MLA_ERR_ARG;
   if (fused ? (w_uv == nullptr || out == nullptr) : (o_latent == nullptr)) return MLA_ERR_ARG;
@@ -161,6 +162,8 @@ static mla_status attend_common(int mode, const uint16_t *q_tilde, const uint16_
   p.max_pages = max_pages;
   p.num_pages = num_pages;
   p.K = K;
+  p.window = window;
+  p.sinks = sinks;
   if (mode == kModeIndexed) {
     // Every list has the same tile count, so a group count that is a multiple of the number
     // of lists splits each list into equal parts and no CTA straddles two lists (one
@@ -251,8 +254,8 @@ static mla_status attend_packed_common(const uint16_t *q_tilde, const uint8_t *p
   p.a.lse = lse;
   p.a.status = status;
   p.q_tilde = q_tilde;
-  p.window = window;
-  p.sinks = sinks;
+  p.a.window = window;
+  p.a.sinks = sinks;
   p.unit = unit;
   p.score_factor = scale * 1.4426950408889634f * unit;
   return cuda_status(launch_attend_packed(tm_codes, tm_scales, p, reinterpret_cast<cudaStream_t>(stream)));
@@ -377,6 +380,27 @@ const char *mla_status_string(mla_status s) {
 mla_status mla_absorb_q(const uint16_t *q, const uint16_t *w_uk, uint16_t *q_tilde, int n, int H, int D, int R,
                         void *stream) {
   return mla::proj_common(true, q, w_uk, q_tilde, n, H, D, R, stream);
+}
+
+mla_status mla_attend_window_dense(const uint16_t *q_tilde, const uint16_t *cache, const int32_t *seq_lens, int B, int Q,
+                                   int H, int R, int Lmax, float scale, int window, int sinks, void *workspace,
+                                   size_t ws_bytes, uint16_t *o_latent, float *lse, int32_t *status, void *stream) {
+  if (window < 1 || sinks < 0) return MLA_ERR_ARG;
+  if (Lmax >= (1LL << 31) - 64) return MLA_ERR_ARG;  // tile ends are int32
+  return mla::attend_common(mla::kModeDense, q_tilde, cache, nullptr, nullptr, seq_lens, B, Q, H, R, Lmax, 0, 0, 0, 0,
+                            scale, workspace, ws_bytes, o_latent, lse, status, stream, nullptr, 0, nullptr, window,
+                            sinks);
+}
+
+mla_status mla_attend_window_paged(const uint16_t *q_tilde, const uint16_t *pool, const int32_t *page_table,
+                                   const int32_t *seq_lens, int B, int Q, int H, int R, int page_size, int max_pages,
+                                   int num_pages, float scale, int window, int sinks, void *workspace, size_t ws_bytes,
+                                   uint16_t *o_latent, float *lse, int32_t *status, void *stream) {
+  if (window < 1 || sinks < 0) return MLA_ERR_ARG;
+  if ((long long)max_pages * mla::kPageTokens >= (1LL << 31) - 64) return MLA_ERR_ARG;
+  return mla::attend_common(mla::kModePaged, q_tilde, pool, page_table, nullptr, seq_lens, B, Q, H, R, 0, page_size,
+                            max_pages, num_pages, 0, scale, workspace, ws_bytes, o_latent, lse, status, stream, nullptr,
+                            0, nullptr, window, sinks);
 }
 
 mla_status mla_attend_packed(const uint16_t *q_tilde, const uint8_t *pool, const int32_t *page_table,

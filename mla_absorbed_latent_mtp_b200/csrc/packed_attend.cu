@@ -151,7 +151,7 @@ __device__ __forceinline__ int seq_len(const AttendPackedParams &p, int b) {
   return min(max(p.a.seq_lens[b], 0), p.a.max_pages * kPageTokens);
 }
 __device__ __forceinline__ int seq_tiles(const AttendPackedParams &p, int b) {
-  return SeqTiles(seq_len(p, b), p.a.Q, p.window, p.sinks).count;
+  return SeqTiles(seq_len(p, b), p.a.Q, p.a.window, p.a.sinks).count;
 }
 
 __device__ long long warp_total_tiles(const AttendPackedParams &p, int lane) {
@@ -205,7 +205,7 @@ struct SegIter {
       nt = seq_tiles(p, s);
     }
     sg.b = s;
-    sg.q = QueryTiles(seq_len(p, s), p.a.Q, iq, p.window, p.sinks);
+    sg.q = QueryTiles(seq_len(p, s), p.a.Q, iq, p.a.window, p.a.sinks);
     sg.lo = (int)(t - base);
     const long long end = min(t_end - base, (long long)nt);
     sg.hi = min((int)end, sg.q.e);
