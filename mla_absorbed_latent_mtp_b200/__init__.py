@@ -110,14 +110,31 @@ def status_string(code: int) -> str:
     return lib().mla_status_string(code).decode()
 
 
+_torch = None
+_DTYPES = {}
+
+
+def _get_torch():
+    """torch, imported at the first call that needs it; also fills the dtype table."""
+    global _torch
+    if _torch is None:
+        import torch
+        _DTYPES.update(bf16=torch.bfloat16, i32=torch.int32, f32=torch.float32, u8=torch.uint8)
+        _torch = torch
+    return _torch
+
+
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    """The raw handle of `stream`, or of the current stream of the current device."""
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _get_torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object
+    return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
 
 
 def _check(fn, code):
@@ -130,12 +147,21 @@ def _check_cuda(*tensors):
     for t in tensors:
         if t is None:
             continue
-        if not t.is_cuda:
-            raise ValueError("tensors must be CUDA tensors")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors must be on one device ({dev} and {t.device})")
+        d = t.get_device()
+        if d != dev:
+            if not t.is_cuda:
+                raise ValueError("tensors must be CUDA tensors")
+            if dev is not None:
+                raise ValueError(f"tensors must be on one device (cuda:{dev} and cuda:{d})")
+            dev = d
+    return dev
+
+
+def _check_current(*tensors):
+    """_check_cuda, and that the device is the current one: the kernels are launched there."""
+    dev = _check_cuda(*tensors)
+    if dev != _get_torch().cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{_torch.cuda.current_device()}")
 
 
 def _require(t, name, dtype, shape=None, min_numel=None, optional=False):
@@ -143,20 +169,27 @@ def _require(t, name, dtype, shape=None, min_numel=None, optional=False):
     would let a kernel read or write outside it: the kernels address memory only from the
     pointer and the sizes passed, so a strided, narrower or smaller tensor must never get
     that far.  ``shape`` may hold None for a free dimension."""
-    import torch
     if t is None:
         if optional:
             return
         raise ValueError(f"{name} is required")
-    want = {"bf16": torch.bfloat16, "i32": torch.int32, "f32": torch.float32, "u8": torch.uint8}[dtype]
+    if not _DTYPES:
+        _get_torch()
+    want = _DTYPES[dtype]
     if t.dtype != want:
         raise ValueError(f"{name} must be {want}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if shape is not None:
-        if t.dim() != len(shape) or any(w is not None and int(g) != int(w) for g, w in zip(t.shape, shape)):
+        got = t.shape
+        ok = len(got) == len(shape)
+        if ok:
+            for g, w in zip(got, shape):
+                if w is not None and g != w:
+                    ok = False
+        if not ok:
             raise ValueError(f"{name} must have shape {tuple('*' if w is None else w for w in shape)}, "
-                             f"got {tuple(t.shape)}")
+                             f"got {tuple(got)}")
     if min_numel is not None and t.numel() < min_numel:
         raise ValueError(f"{name} needs at least {min_numel} elements, got {t.numel()}")
 
@@ -169,14 +202,14 @@ def mla_attend_workspace_bytes(B: int, Q: int, heads: int = H, latent: int = R) 
 
 def new_workspace(B: int, Q: int):
     """Allocate (with torch) the workspace the attend calls need."""
-    import torch
+    torch = _get_torch()
     n = mla_attend_workspace_bytes(B, Q)
     return torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
 
 
 def mla_absorb_q(q, w_uk, q_tilde=None, stream=None):
     """q [n, H, D] or [B, Q, H, D] bf16, w_uk [H, D, R] bf16 -> q_tilde [..., H, R] bf16."""
-    import torch
+    torch = _get_torch()
     _require(q, "q", "bf16")
     if q.dim() < 3 or tuple(q.shape[-2:]) != (H, D):
         raise ValueError(f"q must be [..., {H}, {D}], got {tuple(q.shape)}")
@@ -192,7 +225,7 @@ def mla_absorb_q(q, w_uk, q_tilde=None, stream=None):
 
 def mla_up_proj(o_latent, w_uv, out=None, stream=None):
     """o_latent [..., H, R] bf16, w_uv [H, D, R] bf16 -> out [..., H, D] bf16."""
-    import torch
+    torch = _get_torch()
     _require(o_latent, "o_latent", "bf16")
     if o_latent.dim() < 3 or tuple(o_latent.shape[-2:]) != (H, R):
         raise ValueError(f"o_latent must be [..., {H}, {R}], got {tuple(o_latent.shape)}")
@@ -220,7 +253,7 @@ def _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens, seq_lens_
 
 
 def _attend_outputs(q_tilde, o_latent, lse, want_lse):
-    import torch
+    torch = _get_torch()
     B, Q = q_tilde.shape[0], q_tilde.shape[1]
     if o_latent is None:
         o_latent = torch.empty(B, Q, H, R, dtype=torch.bfloat16, device=q_tilde.device)
@@ -305,7 +338,7 @@ def mla_attend_window_dense(q_tilde, cache, window, sinks=0, seq_lens=None, scal
     _require(cache, "cache", "bf16", (None, None, R))
     if cache.shape[0] < B:
         raise ValueError(f"cache holds {cache.shape[0]} sequences, q_tilde {B}")
-    _check_cuda(q_tilde, cache, seq_lens, workspace, o_latent, lse, status)
+    _check_current(q_tilde, cache, seq_lens, workspace, o_latent, lse, status)
     workspace = new_workspace(B, Q) if workspace is None else workspace
     o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
     _check("mla_attend_window_dense", lib().mla_attend_window_dense(
@@ -322,7 +355,7 @@ def mla_attend_window_paged(q_tilde, pool, page_table, seq_lens, window, sinks=0
     _require(page_table, "page_table", "i32", (None, None))
     if page_table.shape[0] < B:
         raise ValueError(f"page_table has {page_table.shape[0]} rows, q_tilde {B} sequences")
-    _check_cuda(q_tilde, pool, page_table, seq_lens, workspace, o_latent, lse, status)
+    _check_current(q_tilde, pool, page_table, seq_lens, workspace, o_latent, lse, status)
     workspace = new_workspace(B, Q) if workspace is None else workspace
     o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
     _check("mla_attend_window_paged", lib().mla_attend_window_paged(
@@ -333,7 +366,7 @@ def mla_attend_window_paged(q_tilde, pool, page_table, seq_lens, window, sinks=0
 
 
 def _fused_outputs(q_tilde, w_uv, out, o_latent, lse, want_lse):
-    import torch
+    torch = _get_torch()
     B, Q = q_tilde.shape[0], q_tilde.shape[1]
     _require(w_uv, "w_uv", "bf16", (H, D, R))
     _require(out, "out", "bf16", (B, Q, H, D), optional=True)
@@ -401,7 +434,7 @@ def mla_attend_up_indexed(q_tilde, cache, indices, w_uv, seq_lens=None, scale=SC
 
 def mla_expand_kv(c, w_uk, w_uv, k=None, v=None, stream=None):
     """Keys and values of every head from the latents: c [..., R] bf16 -> k, v [..., H, D]."""
-    import torch
+    torch = _get_torch()
     _require(c, "c", "bf16")
     if c.dim() < 1 or c.shape[-1] != R:
         raise ValueError(f"c must be [..., {R}], got {tuple(c.shape)}")
@@ -421,7 +454,7 @@ def mla_expand_kv(c, w_uk, w_uv, k=None, v=None, stream=None):
 
 def mla_prefill_expanded(q, k, v, scale=SCALE, out=None, lse=None, status=None, want_lse=True, stream=None):
     """Causal self-attention of B sequences of L tokens: q, k, v [B, L, H, D] bf16 -> out (and lse)."""
-    import torch
+    torch = _get_torch()
     _require(q, "q", "bf16", (None, None, H, D))
     B, L = int(q.shape[0]), int(q.shape[1])
     _require(k, "k", "bf16", (B, L, H, D))
@@ -440,7 +473,7 @@ def mla_prefill_expanded(q, k, v, scale=SCALE, out=None, lse=None, status=None, 
 
 def mla_debug_gather(mode, src, req, page_table=None, indices=None, B=None, Q=1, Lmax=0, status=None, stream=None):
     """Rows the attend kernels would address for requests req [n, 3] int32 (b, i, k)."""
-    import torch
+    torch = _get_torch()
     _require(src, "src", "bf16", (None, None, R))
     _require(req, "req", "i32", (None, 3))
     _require(page_table, "page_table", "i32", (None, None), optional=mode != MODE_PAGED)
@@ -533,7 +566,7 @@ def mla_cache_append_packed(pool, page_table, seq_lens, rows, unit=1.0, status=N
     B, Q = rows.shape[0], rows.shape[1]
     _check_packed(pool, page_table, B, "rows", status)
     _require(seq_lens, "seq_lens", "i32", min_numel=B)
-    _check_cuda(pool, page_table, seq_lens, rows, status)
+    _check_current(pool, page_table, seq_lens, rows, status)
     _check("mla_cache_append_packed", lib().mla_cache_append_packed(
         _ptr(pool), _ptr(page_table), _ptr(seq_lens), _ptr(rows), B, Q, R, PAGE, page_table.shape[1], pool.shape[0],
         unit, _ptr(status), _stream(stream)))
@@ -545,7 +578,7 @@ def mla_cache_truncate_packed(pool, page_table, seq_lens, keep, q_len, status=No
     B = seq_lens.shape[0]
     _require(keep, "keep", "i32", min_numel=B)
     _check_packed(pool, page_table, B, "seq_lens", status)
-    _check_cuda(pool, page_table, seq_lens, keep, status)
+    _check_current(pool, page_table, seq_lens, keep, status)
     _check("mla_cache_truncate_packed", lib().mla_cache_truncate_packed(
         _ptr(pool), _ptr(page_table), _ptr(seq_lens), _ptr(keep), B, q_len, R, PAGE, page_table.shape[1],
         pool.shape[0], _ptr(status), _stream(stream)))
@@ -553,12 +586,12 @@ def mla_cache_truncate_packed(pool, page_table, seq_lens, keep, q_len, status=No
 
 def mla_cache_unpack(pool, page_table, start, n, unit=1.0, rows=None, status=None, stream=None):
     """The values of positions start[b] .. start[b] + n - 1 of a 4-bit pool: rows [B, n, R] bf16."""
-    import torch
+    torch = _get_torch()
     _require(start, "start", "i32", (None,))
     B = start.shape[0]
     _check_packed(pool, page_table, B, "start", status)
     _require(rows, "rows", "bf16", (B, n, R), optional=True)
-    _check_cuda(pool, page_table, start, rows, status)
+    _check_current(pool, page_table, start, rows, status)
     if rows is None:
         rows = torch.empty(B, n, R, dtype=torch.bfloat16, device=pool.device)
     _check("mla_cache_unpack", lib().mla_cache_unpack(
@@ -573,7 +606,7 @@ def mla_attend_packed(q_tilde, pool, page_table, seq_lens, unit=1.0, window=0, s
     `window` rows and the first `sinks` ones."""
     B, Q = _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens, seq_lens_required=True)
     _check_packed(pool, page_table, B, "q_tilde", status)
-    _check_cuda(q_tilde, pool, page_table, seq_lens, workspace, o_latent, lse, status)
+    _check_current(q_tilde, pool, page_table, seq_lens, workspace, o_latent, lse, status)
     workspace = new_workspace(B, Q) if workspace is None else workspace
     o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
     _check("mla_attend_packed", lib().mla_attend_packed(
@@ -589,7 +622,7 @@ def mla_pages_workspace_bytes(n: int, num_pages: int) -> int:
 
 def new_pages_workspace(n: int, num_pages: int):
     """Allocate (with torch) the workspace the page calls need for n sequences or forks."""
-    import torch
+    torch = _get_torch()
     return torch.empty(max(mla_pages_workspace_bytes(n, num_pages), 16), dtype=torch.uint8, device="cuda")
 
 
@@ -617,7 +650,7 @@ def mla_pages_reserve(pool, page_table, seq_lens, refs, q_len, workspace=None, s
     _check_pages(page_table, refs, status, seq_lens)
     B, max_pages = page_table.shape
     page_bytes = _check_page_pool(pool, refs, B, workspace)
-    _check_cuda(pool, page_table, seq_lens, refs, workspace, status)
+    _check_current(pool, page_table, seq_lens, refs, workspace, status)
     workspace = new_pages_workspace(B, pool.shape[0]) if workspace is None else workspace
     _check("mla_pages_reserve", lib().mla_pages_reserve(
         _ptr(pool), page_bytes, _ptr(page_table), _ptr(seq_lens), _ptr(refs), B, q_len, max_pages, pool.shape[0],
@@ -632,7 +665,7 @@ def mla_pages_fork(pool, page_table, seq_lens, refs, parents, children, workspac
     _require(children, "children", "i32", (n,))
     B, max_pages = page_table.shape
     page_bytes = _check_page_pool(pool, refs, n, workspace)
-    _check_cuda(pool, page_table, seq_lens, refs, parents, children, workspace, status)
+    _check_current(pool, page_table, seq_lens, refs, parents, children, workspace, status)
     workspace = new_pages_workspace(n, pool.shape[0]) if workspace is None else workspace
     _check("mla_pages_fork", lib().mla_pages_fork(
         _ptr(pool), page_bytes, _ptr(page_table), _ptr(seq_lens), _ptr(refs), _ptr(parents), _ptr(children), n, B,
@@ -642,7 +675,7 @@ def mla_pages_fork(pool, page_table, seq_lens, refs, parents, children, workspac
 def mla_pages_release(page_table, seq_lens, refs, status=None, stream=None):
     """Unmap the entries behind each sequence's last row (all of them where its length is 0)."""
     _check_pages(page_table, refs, status, seq_lens)
-    _check_cuda(page_table, seq_lens, refs, status)
+    _check_current(page_table, seq_lens, refs, status)
     _check("mla_pages_release", lib().mla_pages_release(
         _ptr(page_table), _ptr(seq_lens), _ptr(refs), page_table.shape[0], page_table.shape[1], refs.numel(),
         _ptr(status), _stream(stream)))
@@ -650,11 +683,11 @@ def mla_pages_release(page_table, seq_lens, refs, status=None, stream=None):
 
 def mla_pages_compact(pool, page_table, refs, n_used=None, workspace=None, status=None, stream=None):
     """Move the used pages to the front of the pool; returns n_used [1] int32, their number."""
-    import torch
+    torch = _get_torch()
     _check_pages(page_table, refs, status, lens_required=False)
     _require(n_used, "n_used", "i32", min_numel=1, optional=True)
     page_bytes = _check_page_pool(pool, refs, 1, workspace)
-    _check_cuda(pool, page_table, refs, n_used, workspace, status)
+    _check_current(pool, page_table, refs, n_used, workspace, status)
     if n_used is None:
         n_used = torch.empty(1, dtype=torch.int32, device=pool.device)
     workspace = new_pages_workspace(1, pool.shape[0]) if workspace is None else workspace
@@ -673,7 +706,7 @@ def mla_debug_wait_timeout(limit_cycles, status, stream=None):
 
 def mla_kpool_keys(cache, pool, seq_lens=None, pooled=None, stream=None):
     """Pooled keys [B, Lmax // pool, R] fp32 of every complete pool of cache [B, Lmax, R]."""
-    import torch
+    torch = _get_torch()
     _require(cache, "cache", "bf16", (None, None, R))
     B, Lmax = cache.shape[0], cache.shape[1]
     _require(seq_lens, "seq_lens", "i32", min_numel=B, optional=True)
@@ -690,7 +723,7 @@ def mla_kpool_keys(cache, pool, seq_lens=None, pooled=None, stream=None):
 
 def mla_kpool_select(pooled, w_query, pool, topk, seq_lens=None, with_tail=True, Lmax=None, stream=None):
     """Index lists [B, Q, topk (+ pool - 1)] int32 for w_query [B, Q, R] bf16."""
-    import torch
+    torch = _get_torch()
     _require(w_query, "w_query", "bf16", (None, None, R))
     B, Q = w_query.shape[0], w_query.shape[1]
     _require(pooled, "pooled", "f32", (B, None, R))

@@ -58,6 +58,12 @@ constexpr int kSoftmaxWarps = 8;
 constexpr float kTau = 8.f;                     // the running max is raised when a score exceeds it by this
 constexpr float kShift = 7.f;                   // P is stored as 2^7 p
 
+// A CTA's range of the tile list, and the sequence that holds its first tile.
+struct Range {
+  long long t0, t1, base;  // base: first tile of sequence s
+  int s;
+};
+
 constexpr int kOffQ = kRawSlots * kRawBytes;
 constexpr int kOffP = kOffQ + 8 * kQChunkBytes;
 constexpr int kOffRed = kOffP + 2 * kPBytes;    // [4][64] floats
@@ -73,7 +79,8 @@ constexpr int kBarRawFull = 0, kBarRawEmpty = kBarRawFull + kRawSlots, kBarSAFul
               kBarOFull = kBarPEmpty + 2, kBarOEmpty = kBarOFull + 1, kBarDrain = kBarOEmpty + 1,
               kNumBars = kBarDrain + 1;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
-constexpr int kSmemBytes = kOffMisc + 16 + 1024;  // slack for 1024-byte alignment of the base
+constexpr int kOffRange = kOffMisc + 16;
+constexpr int kSmemBytes = kOffRange + (int)sizeof(Range) + 1024;  // slack for 1024-byte alignment of the base
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 // Tensor memory columns.
@@ -154,12 +161,46 @@ __device__ __forceinline__ int seq_tiles(const AttendPackedParams &p, int b) {
   return SeqTiles(seq_len(p, b), p.a.Q, p.a.window, p.a.sinks).count;
 }
 
-__device__ long long warp_total_tiles(const AttendPackedParams &p, int lane) {
-  long long acc = 0;
-  for (int s = lane; s < p.a.B; s += 32) acc += seq_tiles(p, s);
+// floor(g T / G), in 32 bits where the list allows it.
+__device__ __forceinline__ long long group_start(int g, long long T, int G) {
+  if (T >= (1LL << 31)) return split::group_start(g, T, G);
+  const uint32_t q = (uint32_t)T / (uint32_t)G, r = (uint32_t)T % (uint32_t)G;
+  return (long long)g * q + (uint32_t)g * r / (uint32_t)G;  // G is at most the number of SMs
+}
+
+// By one warp, with an inclusive scan in steps of 32 sequences (a walk from the first sequence cost
+// the last CTAs of a 32-sequence step a microsecond).
+__device__ Range find_range(const AttendPackedParams &p, int g, int lane) {
+  auto scan = [&](int s0, int &nt) {
+    nt = s0 + lane < p.a.B ? seq_tiles(p, s0 + lane) : 0;
+    int x = nt;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-  return acc;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  };
+  long long T = 0;
+  int nt, x = 0;
+  for (int s0 = 0; s0 < p.a.B; s0 += 32) {
+    x = scan(s0, nt);
+    T += __shfl_sync(0xffffffffu, x, 31);
+  }
+  Range r = {group_start(g, T, p.a.groups), group_start(g + 1, T, p.a.groups), 0, 0};
+  if (r.t0 >= r.t1) return r;
+  for (int s0 = 0; s0 < p.a.B; s0 += 32) {
+    if (p.a.B > 32) x = scan(s0, nt);
+    const uint32_t behind = __ballot_sync(0xffffffffu, r.base + x > r.t0);  // the range starts before their end
+    if (behind) {
+      const int l = __ffs(behind) - 1;
+      r.s = s0 + l;
+      r.base += __shfl_sync(0xffffffffu, x - nt, l);
+      break;
+    }
+    r.base += __shfl_sync(0xffffffffu, x, 31);
+  }
+  return r;
 }
 
 __device__ void warp_write_seq_prefix(const AttendPackedParams &p, int lane) {
@@ -195,7 +236,7 @@ struct Segment {
 struct SegIter {
   long long t, t_end, base;
   int s, iq;
-  __device__ SegIter(long long t0, long long t1, int iq_) : t(t0), t_end(t1), base(0), s(0), iq(iq_) {}
+  __device__ SegIter(const Range &r, int iq_) : t(r.t0), t_end(r.t1), base(r.base), s(r.s), iq(iq_) {}
   __device__ bool next(const AttendPackedParams &p, Segment &sg) {
     if (t >= t_end) return false;
     int nt = seq_tiles(p, s);
@@ -219,6 +260,7 @@ struct Shared {
   uint8_t *base;
   uint64_t *bar;
   float *red, *m, *alpha, *rise, *cs;
+  const Range *range;
   uint32_t *tmem_slot;
   volatile int *abort_flag;
 };
@@ -269,53 +311,69 @@ struct Ring {
   }
 };
 
-// ------------------------------------------------------------------ loads (warp 0, one lane)
+// ------------------------------------------------------------------ loads (warp 0)
+// The warp reads the page ids of 16 tiles at a time, lane 0 issues the copies.  A page without a
+// visible row is not loaded (it need not be mapped).
 __device__ void producer_role(const AttendPackedParams &p, const Shared &sh, const CUtensorMap *tm_codes,
-                              const CUtensorMap *tm_scales, int iq, long long t0, long long t1) {
-  uint64_t *bar = sh.bar;
+                              const CUtensorMap *tm_scales, int iq, int lane) {
+  const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.a.status};
   Ring raw;
   uint32_t issued = 0;
-  bool ok = true;
-  SegIter it(t0, t1, iq);
+  SegIter it(*sh.range, iq);
   Segment sg;
-  while (ok && it.next(p, sg)) {
-    for (int n = sg.first(); ok && n < sg.hi; n = sg.next(n)) {
-      ok = mbar_wait(&bar[kBarRawEmpty + raw.slot], raw.phase ^ 1, sh.abort_flag, p.a.status);
-      if (!ok) break;
-      const int j0 = sg.q.seq.tile(n) * kTile;
-      uint8_t *dst = sh.base + raw.slot * kRawBytes;
-      uint64_t *full = &bar[kBarRawFull + raw.slot];
-      // a page without a visible row is not loaded (it need not be mapped)
-      const bool use0 = sg.q.any_row(j0, kPageTokens), use1 = sg.q.any_row(j0 + kPageTokens, kPageTokens);
-      mbar_arrive_expect_tx(full, ((use0 ? 1 : 0) + (use1 ? 1 : 0)) * kPageBytes);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (!(h ? use1 : use0)) continue;
-        int page = p.a.page_table[(long long)sg.b * p.a.max_pages + j0 / kPageTokens + h];
-        if (page < 0 || page >= p.a.num_pages) {
-          report_status(p.a.status, kStatusIndex);
-          page = 0;
+  while (it.next(p, sg)) {
+    const int32_t *table = p.a.page_table + (long long)sg.b * p.a.max_pages;
+    const int count = sg.count();
+    int n = sg.first();
+    for (int k0 = 0; k0 < count; k0 += 16) {
+      // lane: page lane % 2 of the tile lane / 2 further on (past tile a the list goes on at b)
+      int ahead = n + lane / 2;
+      if (n < sg.q.a && ahead >= sg.q.a) ahead += sg.q.b - sg.q.a;
+      int id = -1;  // not loaded
+      if (k0 + lane / 2 < count) {
+        const int pg = sg.q.seq.tile(ahead) * (kTile / kPageTokens) + lane % 2;
+        if (sg.q.any_row(pg * kPageTokens, kPageTokens)) {
+          id = table[pg];
+          if (id < 0 || id >= p.a.num_pages) {
+            report_status(p.a.status, kStatusIndex);
+            id = 0;
+          }
         }
-        tma_load_3d(dst + h * (kHalfBytes / 2), tm_codes, full, 0, page * kPageTokens, 0);
-        tma_load_3d(dst + kHalfBytes + h * (kHalfBytes / 2), tm_codes, full, 0, page * kPageTokens, 1);
-        tma_load_2d(dst + kRawCodeBytes + h * kPageScaleBytes, tm_scales, full, 0, page * kPageTokens);
       }
-      raw.step(kRawSlots);
-      ++issued;
+      for (int k = 0; k < 16 && k0 + k < count; ++k, n = sg.next(n)) {
+        const int page[2] = {__shfl_sync(0xffffffffu, id, 2 * k), __shfl_sync(0xffffffffu, id, 2 * k + 1)};
+        if (!wait_warp(bar, kBarRawEmpty + raw.slot, raw.phase ^ 1)) goto done;
+        if (lane == 0) {
+          uint8_t *dst = sh.base + raw.slot * kRawBytes;
+          uint64_t *full = &sh.bar[kBarRawFull + raw.slot];
+          mbar_arrive_expect_tx(full, ((page[0] >= 0) + (page[1] >= 0)) * kPageBytes);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (page[h] < 0) continue;
+            const int row = page[h] * kPageTokens;
+            tma_load_3d(dst + h * (kHalfBytes / 2), tm_codes, full, 0, row, 0);
+            tma_load_3d(dst + kHalfBytes + h * (kHalfBytes / 2), tm_codes, full, 0, row, 1);
+            tma_load_2d(dst + kRawCodeBytes + h * kPageScaleBytes, tm_scales, full, 0, row);
+          }
+        }
+        __syncwarp();
+        raw.step(kRawSlots);
+        ++issued;
+      }
     }
   }
-  if (!drain_ring(&bar[kBarRawFull], kRawSlots, issued)) report_status(p.a.status, kStatusTimeout);
+done:
+  if (lane == 0 && !drain_ring(&sh.bar[kBarRawFull], kRawSlots, issued)) report_status(p.a.status, kStatusTimeout);
 }
 
 // ------------------------------------------------------------------ MMA issuers (warps 1 and 2)
-__device__ void score_mma_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, long long t0,
-                               long long t1) {
+__device__ void score_mma_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq) {
   const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.a.status};
   constexpr uint32_t idesc = idesc_f16_f32(kTile, kHeads, false);
   const uint64_t b0 = sw128_desc(smem_u32(sh.base + kOffQ), 16, 1024);
   Ring st;
   uint32_t tiles = 0, segs = 0;
-  SegIter it(t0, t1, iq);
+  SegIter it(*sh.range, iq);
   Segment sg;
   while (it.next(p, sg)) {
     const int count = sg.count();
@@ -344,14 +402,13 @@ __device__ void score_mma_role(const AttendPackedParams &p, const Shared &sh, ui
   }
 }
 
-__device__ void value_mma_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, long long t0,
-                               long long t1) {
+__device__ void value_mma_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq) {
   const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.a.status};
   constexpr uint32_t idesc = idesc_f16_f32(128, kHeads, true);
   const uint64_t b0 = sw128_desc(smem_u32(sh.base + kOffP), kPBytes, 1024);
   Ring st;
   uint32_t tiles = 0, segs = 0;
-  SegIter it(t0, t1, iq);
+  SegIter it(*sh.range, iq);
   Segment sg;
   while (it.next(p, sg)) {
     const int count = sg.count();
@@ -410,8 +467,7 @@ struct Stager {
 };
 
 // Thread = row.  A chunk is 64 latents: 32 bytes of codes, four scales, 32 columns.
-__device__ void unpack_rows_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, long long t0,
-                                 long long t1, int wq, int lane) {
+__device__ void unpack_rows_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, int wq, int lane) {
   const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.a.status};
   const int row = wq * 32 + lane;
   const uint32_t raw0 = smem_u32(sh.base);
@@ -419,7 +475,7 @@ __device__ void unpack_rows_role(const AttendPackedParams &p, const Shared &sh, 
   const uint32_t t_dst = tmem + ((uint32_t)(wq * 32) << 16) + kTmemSA;
   Ring raw;
   Stager out{bar, kBarSAFull, kBarSAEmpty, Ring()};
-  SegIter it(t0, t1, iq);
+  SegIter it(*sh.range, iq);
   Segment sg;
   while (it.next(p, sg)) {
     for (int n = sg.first(); n < sg.hi; n = sg.next(n)) {
@@ -469,8 +525,7 @@ __device__ __forceinline__ int k_of_row(int r) {  // K index of tile row r
   return (r & ~15) | ((r & 6) << 1) | ((r & 8) >> 2) | (r & 1);
 }
 
-__device__ void unpack_latents_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, long long t0,
-                                    long long t1, int wq, int lane) {
+__device__ void unpack_latents_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, int wq, int lane) {
   const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.a.status};
   const int g = lane >> 2, c = lane & 3;
   const int group = 8 * wq + g;
@@ -484,7 +539,7 @@ __device__ void unpack_latents_role(const AttendPackedParams &p, const Shared &s
   const uint32_t t_dst = tmem + ((uint32_t)(wq * 32) << 16) + kTmemVA;
   Ring raw;
   Stager out{bar, kBarVAFull, kBarVAEmpty, Ring()};
-  SegIter it(t0, t1, iq);
+  SegIter it(*sh.range, iq);
   Segment sg;
   while (it.next(p, sg)) {
     for (int n = sg.first(); n < sg.hi; n = sg.next(n)) {
@@ -609,8 +664,7 @@ __device__ __forceinline__ float sum_columns(float (&v)[32], int lane) {
   return v[0];
 }
 
-__device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int grp, int iq,
-                             long long t0, long long t1, int warp, int lane) {
+__device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int grp, int iq, int warp, int lane) {
   const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.a.status};
   const int w = warp - 3, wg = w >> 2, wq = warp & 3;
   const int tid = wq * 32 + lane;    // within the warpgroup
@@ -623,7 +677,7 @@ __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint
   const float4 *cs4 = reinterpret_cast<const float4 *>(sh.cs + col0);
   const float4 *m4 = reinterpret_cast<const float4 *>(sh.m + col0);
   uint32_t tiles = 0, segs = 0;
-  SegIter it(t0, t1, iq);
+  SegIter it(*sh.range, iq);
   Segment sg;
   while (it.next(p, sg)) {
     const long long slot = split::partial_slot(p.a, kModePaged, grp, sg.b, iq);
@@ -776,6 +830,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   sh.alpha = reinterpret_cast<float *>(sh.base + kOffAlpha);
   sh.rise = reinterpret_cast<float *>(sh.base + kOffRise);
   sh.cs = reinterpret_cast<float *>(sh.base + kOffCs);
+  Range *range = reinterpret_cast<Range *>(sh.base + kOffRange);
+  sh.range = range;
   sh.tmem_slot = reinterpret_cast<uint32_t *>(sh.base + kOffMisc);
   sh.abort_flag = reinterpret_cast<volatile int *>(sh.base + kOffMisc + 4);
 
@@ -814,27 +870,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_dep_launch();
   grid_dep_wait();  // everything below may come from the previous kernel
-  const long long T = warp_total_tiles(p, lane);
-  const long long G = p.a.groups;
-  if (blockIdx.x == 0 && warp == 0) warp_write_seq_prefix(p, lane);
-  const long long t0 = split::group_start(g, T, G), t1 = split::group_start(g + 1, T, G);
+  if (warp == 0) {
+    const Range r = find_range(p, g, lane);
+    if (lane == 0) *range = r;
+  }
+  if (blockIdx.x == 0 && warp == 2) warp_write_seq_prefix(p, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *sh.tmem_slot;
 
   if (warp == 0) {
-    if (lane == 0) producer_role(p, sh, &tm_codes, &tm_scales, iq, t0, t1);
+    producer_role(p, sh, &tm_codes, &tm_scales, iq, lane);
   } else if (warp == 1) {
-    score_mma_role(p, sh, tmem, iq, t0, t1);
+    score_mma_role(p, sh, tmem, iq);
   } else if (warp == 2) {
-    value_mma_role(p, sh, tmem, iq, t0, t1);
+    value_mma_role(p, sh, tmem, iq);
   } else if (warp < 11) {
-    softmax_role(p, sh, tmem, g, iq, t0, t1, warp, lane);
+    softmax_role(p, sh, tmem, g, iq, warp, lane);
   } else if (warp < 15) {
-    unpack_rows_role(p, sh, tmem, iq, t0, t1, warp & 3, lane);
+    unpack_rows_role(p, sh, tmem, iq, warp & 3, lane);
   } else {
-    unpack_latents_role(p, sh, tmem, iq, t0, t1, warp & 3, lane);
+    unpack_latents_role(p, sh, tmem, iq, warp & 3, lane);
   }
 
   __syncwarp();
