@@ -61,7 +61,7 @@ constexpr float kShift = 7.f;                   // P is stored as 2^7 p
 // A CTA's range of the tile list, and the sequence that holds its first tile.
 struct Range {
   long long t0, t1, base;  // base: first tile of sequence s
-  int s;
+  int s, L;                // and its length
 };
 
 constexpr int kOffQ = kRawSlots * kRawBytes;
@@ -157,8 +157,8 @@ __device__ __forceinline__ void add_f32x2(float &d0, float &d1, float a0, float 
 __device__ __forceinline__ int seq_len(const AttendPackedParams &p, int b) {
   return min(max(p.a.seq_lens[b], 0), p.a.max_pages * kPageTokens);
 }
-__device__ __forceinline__ int seq_tiles(const AttendPackedParams &p, int b) {
-  return SeqTiles(seq_len(p, b), p.a.Q, p.a.window, p.a.sinks).count;
+__device__ __forceinline__ int seq_tiles(const AttendPackedParams &p, int L) {
+  return SeqTiles(L, p.a.Q, p.a.window, p.a.sinks).count;
 }
 
 // floor(g T / G), in 32 bits where the list allows it.
@@ -171,8 +171,10 @@ __device__ __forceinline__ long long group_start(int g, long long T, int G) {
 // By one warp, with an inclusive scan in steps of 32 sequences (a walk from the first sequence cost
 // the last CTAs of a 32-sequence step a microsecond).
 __device__ Range find_range(const AttendPackedParams &p, int g, int lane) {
+  int L = 0;
   auto scan = [&](int s0, int &nt) {
-    nt = s0 + lane < p.a.B ? seq_tiles(p, s0 + lane) : 0;
+    L = s0 + lane < p.a.B ? seq_len(p, s0 + lane) : 0;
+    nt = s0 + lane < p.a.B ? seq_tiles(p, L) : 0;
     int x = nt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -187,7 +189,7 @@ __device__ Range find_range(const AttendPackedParams &p, int g, int lane) {
     x = scan(s0, nt);
     T += __shfl_sync(0xffffffffu, x, 31);
   }
-  Range r = {group_start(g, T, p.a.groups), group_start(g + 1, T, p.a.groups), 0, 0};
+  Range r = {group_start(g, T, p.a.groups), group_start(g + 1, T, p.a.groups), 0, 0, 0};
   if (r.t0 >= r.t1) return r;
   for (int s0 = 0; s0 < p.a.B; s0 += 32) {
     if (p.a.B > 32) x = scan(s0, nt);
@@ -195,6 +197,7 @@ __device__ Range find_range(const AttendPackedParams &p, int g, int lane) {
     if (behind) {
       const int l = __ffs(behind) - 1;
       r.s = s0 + l;
+      r.L = __shfl_sync(0xffffffffu, L, l);
       r.base += __shfl_sync(0xffffffffu, x - nt, l);
       break;
     }
@@ -207,7 +210,7 @@ __device__ void warp_write_seq_prefix(const AttendPackedParams &p, int lane) {
   long long base = 0;
   for (int s0 = 0; s0 < p.a.B; s0 += 32) {
     const int s = s0 + lane;
-    const int nt = s < p.a.B ? seq_tiles(p, s) : 0;
+    const int nt = s < p.a.B ? seq_tiles(p, seq_len(p, s)) : 0;
     long long x = nt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -235,18 +238,18 @@ struct Segment {
 };
 struct SegIter {
   long long t, t_end, base;
-  int s, iq;
-  __device__ SegIter(const Range &r, int iq_) : t(r.t0), t_end(r.t1), base(r.base), s(r.s), iq(iq_) {}
+  int s, L, iq;
+  __device__ SegIter(const Range &r, int iq_) : t(r.t0), t_end(r.t1), base(r.base), s(r.s), L(r.L), iq(iq_) {}
   __device__ bool next(const AttendPackedParams &p, Segment &sg) {
     if (t >= t_end) return false;
-    int nt = seq_tiles(p, s);
+    int nt = seq_tiles(p, L);
     while (base + nt <= t) {
       base += nt;
-      ++s;
-      nt = seq_tiles(p, s);
+      L = seq_len(p, ++s);
+      nt = seq_tiles(p, L);
     }
     sg.b = s;
-    sg.q = QueryTiles(seq_len(p, s), p.a.Q, iq, p.a.window, p.a.sinks);
+    sg.q = QueryTiles(L, p.a.Q, iq, p.a.window, p.a.sinks);
     sg.lo = (int)(t - base);
     const long long end = min(t_end - base, (long long)nt);
     sg.hi = min((int)end, sg.q.e);
@@ -870,18 +873,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_dep_launch();
   grid_dep_wait();  // everything below may come from the previous kernel
+  if (blockIdx.x == 0 && warp == 2) warp_write_seq_prefix(p, lane);
   if (warp == 0) {
+    // this warp initialised the barriers and finds the range: it starts loading at once
     const Range r = find_range(p, g, lane);
     if (lane == 0) *range = r;
+    __syncwarp();
+    asm volatile("bar.arrive 0, %0;" ::"n"(kThreads) : "memory");
+    producer_role(p, sh, &tm_codes, &tm_scales, iq, lane);
+  } else {
+    tc_fence_before();
+    asm volatile("bar.sync 0, %0;" ::"n"(kThreads) : "memory");
+    tc_fence_after();
   }
-  if (blockIdx.x == 0 && warp == 2) warp_write_seq_prefix(p, lane);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = *sh.tmem_slot;
 
   if (warp == 0) {
-    producer_role(p, sh, &tm_codes, &tm_scales, iq, lane);
+    // done above
   } else if (warp == 1) {
     score_mma_role(p, sh, tmem, iq);
   } else if (warp == 2) {
