@@ -282,10 +282,10 @@ mla_status mla_cache_truncate_paged(uint16_t *pool, const int32_t *page_table, i
  * mla_cache_append_packed: mla_cache_append_paged with quantisation.  For each group of 16 latents
  *   y = x / unit, scale = e4m3(max|y| / 6) and code = e2m1(y / scale), both to nearest with ties to
  *   even, at most 448 and 6; a scale of zero gives codes of zero; a group that holds an Inf or a NaN
- *   gets the scale NaN.  rows [B, Q, R] bf16, seq_lens in/out; Q <= 4,194,240.
+ *   gets the scale NaN.  rows [B, Q, R] bf16, seq_lens in/out; Q <= 2,097,120.
  * mla_cache_truncate_packed: as mla_cache_truncate_paged; the discarded rows become zero bytes.
  * mla_cache_unpack: rows[b, i] = the bf16 values at position start[b] + i, i < n (exact: a value has
- *   six significant bits), for example for mla_expand_kv.  rows [B, n, R] bf16, start [B] int32.  A
+ *   six significant bits), for example for mla_expand_kv.  rows [B, n, R] bf16, start [B] int32; B <= 65535.  A
  *   position outside the table or on an unmapped page gives a zero row and MLA_ERR_INDEX.
  * mla_attend_packed: attention over the packed rows; window and sinks as for mla_attend_window_*,
  *   window = 0 sees every row up to the query's own.  q_tilde, outputs, workspace as for

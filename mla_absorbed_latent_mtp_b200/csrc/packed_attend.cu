@@ -494,7 +494,7 @@ __device__ void unpack_rows_role(const AttendPackedParams &p, const Shared &sh, 
         sc = ld_shared_u32(base + kRawCodeBytes + row * kScaleBytes + 4 * ch);
       };
       load(0);
-#pragma unroll 1
+#pragma unroll 2
       for (int ch = 0; ch < kChunks; ++ch) {
         const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
         const uint32_t s01 = e4m3x2_to_f16x2(sc & 0xFFFFu), s23 = e4m3x2_to_f16x2(sc >> 16);
@@ -563,7 +563,7 @@ __device__ void unpack_latents_role(const AttendPackedParams &p, const Shared &s
         }
       };
       load(0);
-#pragma unroll 1
+#pragma unroll 2
       for (int ks = 0; ks < kChunks; ++ks) {
         if (!whole) {
 #pragma unroll

@@ -3,9 +3,14 @@
 //
 // Append: 16 latents, one scale group, per thread, a row per warp: 32 bytes in, 8 + 1 out.
 //   y = x / unit,  s = e4m3(max|y| / 6),  code = e2m1(y / s)
-// The divisions are IEEE divisions: a value on the border between two codes (y / s exactly
-// 0.25, 0.75, ...) has to meet the conversion as a tie, which a product with a rounded 1 / s
-// does not give.  unit is a power of two, so y is exact.
+// The codes' borders (0.25, 0.75, ...) are met exactly as ties: y has 8 significant bits and s
+// four, so y / s is a border or at least 2^-8 of it away.  y * (1 / s) is within 2^-22 of y / s;
+// rounding it to a multiple of 2^-11 (the sum with 6144 does, one rounding in the fma) therefore
+// gives the border where y / s is one and crosses none where it is not.  unit is a power of two,
+// so y is exact.
+//
+// What bounds it: memory for many rows (1,024 bytes in and 288 out a row), and for few the chain
+// length -> page table -> store, which is why a warp's loads of two rows are in flight before it.
 #include <algorithm>
 
 #include "internal.h"
@@ -18,7 +23,7 @@ namespace packed {
 
 constexpr int kThreads = 256;
 constexpr int kRowsPerPass = kThreads / 32;
-constexpr int kRowsPerCta = 64;  // rows of a sequence that one CTA appends when there are many
+constexpr int kRowsPerCta = 32;  // rows of a sequence that one CTA appends when there are many
 
 struct Store {
   uint8_t *pool;
@@ -43,14 +48,16 @@ __device__ bool range_ok(const Store &st, int b, long long lo, long long hi) {
   return __syncthreads_and(ok);
 }
 
-__device__ __forceinline__ void append_group(const uint16_t *src, uint8_t *row, int group, float inv_unit) {
-  uint32_t x[8];
-  {
-    const uint4 a = *reinterpret_cast<const uint4 *>(src + group * kGroup);
-    const uint4 b = *reinterpret_cast<const uint4 *>(src + group * kGroup + 8);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  }
+struct Group {
+  uint4 a, b;  // 16 latents, bf16
+};
+__device__ __forceinline__ Group load_group(const uint16_t *src, int group) {
+  const uint4 *at = reinterpret_cast<const uint4 *>(src + group * kGroup);
+  return {at[0], at[1]};
+}
+
+__device__ __forceinline__ void store_group(const Group &g, uint8_t *row, int group, float inv_unit) {
+  const uint32_t x[8] = {g.a.x, g.a.y, g.a.z, g.a.w, g.b.x, g.b.y, g.b.z, g.b.w};
   uint32_t mx = 0;  // the largest |x|, as bf16 bits
 #pragma unroll
   for (int k = 0; k < 8; ++k) mx = max(mx, max(x[k] & 0x7FFFu, (x[k] >> 16) & 0x7FFFu));
@@ -61,13 +68,16 @@ __device__ __forceinline__ void append_group(const uint16_t *src, uint8_t *row, 
     scale = f32_to_e4m3x2(__fdiv_rn(amax, 6.f), 0.f) & 0xFFu;
     const float s = __half2float(__ushort_as_half((unsigned short)(e4m3x2_to_f16x2(scale) & 0xFFFFu)));
     if (s > 0.f) {
-      float v[8];
+      const float per = __frcp_rn(s) * inv_unit;
+      constexpr float kGrid = 6144.f;  // floats there are multiples of 2^-11
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        float v[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[2 * k] = __fdiv_rn(bf16lo_to_f32(x[4 * h + k]) * inv_unit, s);
-          v[2 * k + 1] = __fdiv_rn(bf16hi_to_f32(x[4 * h + k]) * inv_unit, s);
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t w = x[4 * h + k / 2];
+          const float y = k & 1 ? bf16hi_to_f32(w) : bf16lo_to_f32(w);
+          v[k] = copysignf(fmaf(y, per, kGrid) - kGrid, y);  // a zero keeps its sign
         }
         (h ? codes.y : codes.x) = f32x8_to_e2m1(v);
       }
@@ -83,14 +93,26 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const Store st, int32_
                                                           int Q, int rows_per_cta, float inv_unit, int32_t *status) {
   grid_dep_launch();
   grid_dep_wait();
-  const int b = blockIdx.x;
+  const int b = blockIdx.x, lane = threadIdx.x & 31;
+  const int i0 = blockIdx.y * rows_per_cta + (int)(threadIdx.x >> 5), i1 = min(Q, (int)(blockIdx.y + 1) * rows_per_cta);
+  const uint16_t *src = rows + (long long)b * Q * kLatent;
+  Group g[2];  // rows i0 and i0 + kRowsPerPass are on their way before the length is known
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    if (i0 + u * kRowsPerPass < i1) g[u] = load_group(src + (long long)(i0 + u * kRowsPerPass) * kLatent, lane);
   const long long L = seq_lens[b];
   const bool ok = range_ok(st, b, L, L + Q) && L >= 0;
-  const int i0 = blockIdx.y * rows_per_cta, i1 = min(Q, i0 + rows_per_cta);
   if (ok) {
-    const int lane = threadIdx.x & 31;
-    for (int i = i0 + (int)(threadIdx.x >> 5); i < i1; i += kRowsPerPass)
-      append_group(rows + ((long long)b * Q + i) * kLatent, st.pool + row_offset(st, b, L + i), lane, inv_unit);
+    for (int i = i0; i < i1; i += 2 * kRowsPerPass) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int r = i + u * kRowsPerPass, next = r + 2 * kRowsPerPass;
+        if (r >= i1) break;
+        const Group now = g[u];
+        if (next < i1) g[u] = load_group(src + (long long)next * kLatent, lane);
+        store_group(now, st.pool + row_offset(st, b, L + r), lane, inv_unit);
+      }
+    }
   }
   if (gridDim.y == 1) {
     __syncthreads();  // every thread has read the length
@@ -135,38 +157,51 @@ __global__ void __launch_bounds__(kThreads) truncate_kernel(const Store st, int3
   }
 }
 
-// rows[b, i] = the values at position start[b] + i, 16 latents per thread.
-__global__ void __launch_bounds__(kThreads) unpack_kernel(const Store st, const int32_t *start, uint16_t *rows, int B,
-                                                          int n, float unit, int32_t *status) {
+// rows[b, i] = the values at position start[b] + i, 16 latents per thread, two rows of a warp at once.
+__device__ __forceinline__ void write_values(uint16_t *dst, uint2 w, uint32_t scale, float unit) {
+  const uint32_t s = prmt(e4m3x2_to_f16x2(scale), 0, 0x1010u);
+  uint32_t out[8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[4];
+    e2m1x8_to_f16x2(h ? w.y : w.x, v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t y = mul_f16x2(v[k], s);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&y));
+      out[4 * h + k] = pack_bf16x2(f.x * unit, f.y * unit);
+    }
+  }
+  reinterpret_cast<uint4 *>(dst)[0] = make_uint4(out[0], out[1], out[2], out[3]);
+  reinterpret_cast<uint4 *>(dst)[1] = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+__global__ void __launch_bounds__(kThreads) unpack_kernel(const Store st, const int32_t *start, uint16_t *rows, int n,
+                                                          float unit, int32_t *status) {
   grid_dep_launch();
   grid_dep_wait();
-  const int group = threadIdx.x & 31;
-  const long long total = (long long)B * n;
-  for (long long r = (long long)blockIdx.x * kRowsPerPass + (threadIdx.x >> 5); r < total;
-       r += (long long)gridDim.x * kRowsPerPass) {
-    const int b = (int)(r / n), i = (int)(r % n);
-    const long long off = start[b] < 0 ? -1 : row_offset(st, b, (long long)start[b] + i);
-    uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (off < 0) {
-      if (group == 0) report_status(status, kStatusIndex);
-    } else {
-      const uint2 w = *reinterpret_cast<const uint2 *>(st.pool + off + group * 8);
-      const uint32_t s = prmt(e4m3x2_to_f16x2(st.pool[off + kCodeBytes + group]), 0, 0x1010u);
+  const int group = threadIdx.x & 31, b = blockIdx.y;
+  const long long j0 = start[b];
+  uint16_t *out = rows + (long long)b * n * kLatent + group * kGroup;
+  for (int i = blockIdx.x * 2 * kRowsPerPass + (int)(threadIdx.x >> 5); i < n; i += gridDim.x * 2 * kRowsPerPass) {
+    uint2 w[2];
+    uint32_t s[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t v[4];
-        e2m1x8_to_f16x2(h ? w.y : w.x, v);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t y = mul_f16x2(v[k], s);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&y));
-          out[4 * h + k] = pack_bf16x2(f.x * unit, f.y * unit);
-        }
+    for (int u = 0; u < 2; ++u) {
+      const int r = i + u * kRowsPerPass;
+      const long long off = r < n && j0 >= 0 ? row_offset(st, b, j0 + r) : -1;
+      w[u] = make_uint2(0u, 0u);
+      s[u] = 0;
+      if (off >= 0) {
+        w[u] = *reinterpret_cast<const uint2 *>(st.pool + off + group * 8);
+        s[u] = st.pool[off + kCodeBytes + group];
+      } else if (r < n && group == 0) {
+        report_status(status, kStatusIndex);
       }
     }
-    uint4 *dst = reinterpret_cast<uint4 *>(rows + r * kLatent + group * kGroup);
-    dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-    dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (i + u * kRowsPerPass < n) write_values(out + (long long)(i + u * kRowsPerPass) * kLatent, w[u], s[u], unit);
   }
 }
 
@@ -227,10 +262,10 @@ mla_status mla_cache_unpack(const uint8_t *pool, const int32_t *page_table, cons
   if (mla_status s = check(pool, page_table, start, rows, B, n, R, page_size, max_pages, num_pages, unit); s != MLA_OK)
     return s;
   const Store st{const_cast<uint8_t *>(pool), page_table, max_pages, num_pages};
-  const long long ctas = ((long long)B * n + kRowsPerPass - 1) / kRowsPerPass;
-  const int grid = (int)std::min<long long>(ctas, 16LL * device_sm_count());
-  return record_cuda_error(launch_chained(unpack_kernel, dim3(grid), dim3(kThreads), 0,
-                                          reinterpret_cast<cudaStream_t>(stream), st, start, rows, B, n, unit, status));
+  if (B > 65535) return MLA_ERR_UNSUPPORTED;  // grid rows
+  const int grid = std::min((n + 2 * kRowsPerPass - 1) / (2 * kRowsPerPass), 1 << 16);
+  return record_cuda_error(launch_chained(unpack_kernel, dim3(grid, B), dim3(kThreads), 0,
+                                          reinterpret_cast<cudaStream_t>(stream), st, start, rows, n, unit, status));
 }
 
 }  // extern "C"
