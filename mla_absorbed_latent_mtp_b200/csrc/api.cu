@@ -10,6 +10,7 @@
 #include "internal.h"
 #include "packed.cuh"
 #include "packed_attend.h"
+#include "window_attend.h"
 
 namespace mla {
 
@@ -97,7 +98,8 @@ int device_sm_count() {
   return sm_count_for(dev);
 }
 
-// Shared validation and launch for the three attend modes.  With w_uv / out given, the
+// Shared validation and launch for the three attend modes (window > 0, dense and paged: with a
+// sliding window).  With w_uv / out given, the
 // split-L merge runs fused with the up-projection (o_latent optional); without, the combine
 // writes o_latent (required).
 static mla_status attend_common(int mode, const uint16_t *q_tilde, const uint16_t *cache, const int32_t *page_table,
@@ -151,7 +153,7 @@ static mla_status attend_common(int mode, const uint16_t *q_tilde, const uint16_
     const uint32_t box[3] = {64, 64, (uint32_t)R / 64};
     if (!make_map(&tm_qt, q_tilde, 3, dims, strides, box)) return cuda_status(cudaErrorInvalidValue);
   }
-  AttendParams p;
+  WindowParams p;
   p.seq_lens = seq_lens;
   p.page_table = page_table;
   p.indices = indices;
@@ -195,6 +197,7 @@ static mla_status attend_common(int mode, const uint16_t *q_tilde, const uint16_
   p.lse = lse;
   p.status = status;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (window > 0) return cuda_status(launch_attend_window(mode == kModePaged, tm_cache, tm_qt, p, st));
   if (!fused) return cuda_status(launch_attend(mode, tm_cache, tm_qt, p, st));
   CUtensorMap tm_w;
   if (!make_w_uv_map(&tm_w, w_uv)) return cuda_status(cudaErrorInvalidValue);
@@ -254,8 +257,8 @@ static mla_status attend_packed_common(const uint16_t *q_tilde, const uint8_t *p
   p.a.lse = lse;
   p.a.status = status;
   p.q_tilde = q_tilde;
-  p.a.window = window;
-  p.a.sinks = sinks;
+  p.window = window;
+  p.sinks = sinks;
   p.unit = unit;
   p.score_factor = scale * 1.4426950408889634f * unit;
   return cuda_status(launch_attend_packed(tm_codes, tm_scales, p, reinterpret_cast<cudaStream_t>(stream)));

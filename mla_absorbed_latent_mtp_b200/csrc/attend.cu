@@ -24,22 +24,16 @@
 // read once.  The ring holds 2.25 tiles: while the softmax works on tile t, the score
 // GEMM of tile t+1 runs and tile t+2 streams in; the MMA warp issues each tile's value
 // GEMM as soon as its probabilities are ready, which frees its ring slots.
-//
-// Sliding windows (kWin): a sequence's tile list holds only the tiles of its sinks and of its
-// queries' windows (window.cuh), a query walks those of them that it sees, and rows that it
-// does not see are masked in the softmax and zeroed in the landed slot, whatever they hold.
 #include <math.h>
 
 #include <algorithm>
 #include <map>
 #include <mutex>
-#include <type_traits>
 #include <utility>
 
 #include "internal.h"
 #include "sm100.cuh"
 #include "split.cuh"
-#include "window.cuh"
 
 namespace mla {
 namespace attend {
@@ -94,20 +88,15 @@ __device__ __forceinline__ int seq_rows(const AttendParams &p, int mode, int s) 
 }
 using split::group_start;
 using split::num_seqs;
-using SeqTiles = window::SeqTiles<kTile>;
-using QueryTiles = window::QueryTiles<kTile>;
-template <bool kWin>
 __device__ __forceinline__ int seq_tiles(const AttendParams &p, int mode, int s) {
-  if constexpr (kWin) return SeqTiles(seq_rows(p, mode, s), p.Q, p.window, p.sinks).count;
   return (seq_rows(p, mode, s) + kTile - 1) / kTile;
 }
 
 // Total tiles over all sequences (computed by one warp).
-template <bool kWin>
 __device__ long long warp_total_tiles(const AttendParams &p, int mode, int lane) {
   long long acc = 0;
   const int ns = num_seqs(p, mode);
-  for (int s = lane; s < ns; s += 32) acc += seq_tiles<kWin>(p, mode, s);
+  for (int s = lane; s < ns; s += 32) acc += seq_tiles(p, mode, s);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
   return acc;
@@ -115,13 +104,12 @@ __device__ long long warp_total_tiles(const AttendParams &p, int mode, int lane)
 
 // Position of every sequence in the tile list (first tile, tile count), for the combine
 // (computed by one warp with an exclusive scan in steps of 32 sequences).
-template <bool kWin>
 __device__ void warp_write_seq_prefix(const AttendParams &p, int mode, int lane) {
   const int ns = num_seqs(p, mode);
   long long base = 0;
   for (int s0 = 0; s0 < ns; s0 += 32) {
     const int s = s0 + lane;
-    const int nt = s < ns ? seq_tiles<kWin>(p, mode, s) : 0;
+    const int nt = s < ns ? seq_tiles(p, mode, s) : 0;
     long long x = nt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -136,24 +124,11 @@ __device__ void warp_write_seq_prefix(const AttendParams &p, int mode, int lane)
   }
 }
 
-struct NoWindow {};
-template <bool kWin>
 struct Seg {
   int s;       // sequence in the tile list
   int lo, hi;  // tile range within the sequence (clipped to the query's causal window)
   int rows;    // data rows of the sequence
   bool empty;  // no tile of the range is visible to this CTA's query
-  // Sliding windows: lo, hi and the loops' t count list tiles, of which next() skips those that
-  // the query does not see; tile(t) is the tile of the sequence.
-  std::conditional_t<kWin, QueryTiles, NoWindow> q;
-  __device__ __forceinline__ int next(int t) const {
-    if constexpr (kWin) return q.seek(t + 1);
-    return t + 1;
-  }
-  __device__ __forceinline__ int tile(int t) const {
-    if constexpr (kWin) return q.seq.tile(t);
-    return t;
-  }
 };
 
 // Walks the segments of a contiguous range [t, t_end) of the global tile list.  For a
@@ -161,18 +136,17 @@ struct Seg {
 // (0 .. L - Q + iq): tiles past the causal window are neither loaded nor multiplied, which
 // matters when a window holds many queries (a prefill through this path).  A segment left
 // without tiles is returned with `empty` set; its partial is written as empty.
-template <bool kWin>
 struct SegIter {
   long long t, t_end, base;
   int s, iq;
   __device__ SegIter(long long t0, long long t1, int iq_) : t(t0), t_end(t1), base(0), s(0), iq(iq_) {}
-  __device__ bool next(const AttendParams &p, int mode, Seg<kWin> &sg) {
+  __device__ bool next(const AttendParams &p, int mode, Seg &sg) {
     if (t >= t_end) return false;
-    int nt = seq_tiles<kWin>(p, mode, s);
+    int nt = seq_tiles(p, mode, s);
     while (base + nt <= t) {
       base += nt;
       ++s;
-      nt = seq_tiles<kWin>(p, mode, s);
+      nt = seq_tiles(p, mode, s);
     }
     sg.s = s;
     sg.lo = (int)(t - base);
@@ -181,12 +155,7 @@ struct SegIter {
     sg.rows = seq_rows(p, mode, s);
     t = base + hi;
     sg.empty = false;
-    if constexpr (kWin) {
-      sg.q = QueryTiles(sg.rows, p.Q, iq, p.window, p.sinks);
-      sg.lo = sg.q.seek(sg.lo);
-      sg.hi = min(sg.hi, sg.q.e);
-      sg.empty = sg.hi <= sg.lo;
-    } else if (mode != kModeIndexed) {
+    if (mode != kModeIndexed) {
       const int n_vis = sg.rows - p.Q + iq + 1;
       const int vis_tiles = n_vis > 0 ? (n_vis + kTile - 1) / kTile : 0;
       if (sg.hi > vis_tiles) sg.hi = max(vis_tiles, sg.lo);
@@ -257,7 +226,7 @@ __device__ __forceinline__ uint32_t ring_use(uint32_t k) { return k / kSlots; }
 
 // ------------------------------------------------------------------ producer (warp 0)
 // Issues the loads; counts the q~ loads and the ring-slot loads it issued (for the drain).
-template <int kMode, bool kWin>
+template <int kMode>
 // Index lists are gathered by two warps (half 0: warp 0, tile rows 0-31 and the q~ loads;
 // half 1: warp 11, tile rows 32-63); dense and paged tiles by lane 0 of warp 0 (half 0).
 __device__ void producer_loads(const AttendParams &p, const Shared &sh, const CUtensorMap *tm_cache,
@@ -265,8 +234,8 @@ __device__ void producer_loads(const AttendParams &p, const Shared &sh, const CU
                                uint32_t &q_use, uint32_t &slots_issued) {
   uint64_t *bar = sh.bar;
   uint32_t tile_k = 0;
-  SegIter<kWin> it(t0, t1, iq);
-  Seg<kWin> sg;
+  SegIter it(t0, t1, iq);
+  Seg sg;
   while (it.next(p, kMode, sg)) {
     if (sg.empty) continue;
     const int b = (kMode == kModeIndexed) ? sg.s / p.Q : sg.s;
@@ -294,7 +263,7 @@ __device__ void producer_loads(const AttendParams &p, const Shared &sh, const CU
       const int k = sg.lo * kTile + row_lane;
       if (k < p.K) nxt = list[k];
     }
-    for (int t = sg.lo; t < sg.hi; t = sg.next(t), ++tile_k) {
+    for (int t = sg.lo; t < sg.hi; ++t, ++tile_k) {
       if constexpr (kMode == kModeIndexed) {
         // rows past the list end are zero-filled
         const int limit = query_limit(p, b, qi);
@@ -336,7 +305,7 @@ __device__ void producer_loads(const AttendParams &p, const Shared &sh, const CU
           slots_issued = k + 1;
         }
       } else {
-        const int j0 = sg.tile(t) * kTile;
+        const int j0 = t * kTile;
         long long row = 0;
         if constexpr (kMode == kModePaged) {
           bool bad = false;
@@ -361,11 +330,11 @@ __device__ void producer_loads(const AttendParams &p, const Shared &sh, const CU
 
 // The producer role: the loads, then (also after an abort) a wait until every copy it
 // issued has landed.
-template <int kMode, bool kWin>
+template <int kMode>
 __device__ void producer_role(const AttendParams &p, const Shared &sh, const CUtensorMap *tm_cache,
                               const CUtensorMap *tm_qt, int iq, long long t0, long long t1, int lane, int half) {
   uint32_t q_use = 0, slots_issued = 0;
-  producer_loads<kMode, kWin>(p, sh, tm_cache, tm_qt, iq, t0, t1, lane, half, q_use, slots_issued);
+  producer_loads<kMode>(p, sh, tm_cache, tm_qt, iq, t0, t1, lane, half, q_use, slots_issued);
   if constexpr (kMode == kModeIndexed) cp_async_wait_all();  // this lane's row copies
   if (lane == 0) {
     bool ok = drain_ring(&sh.bar[kBarQFull], 1, q_use);
@@ -377,18 +346,9 @@ __device__ void producer_role(const AttendParams &p, const Shared &sh, const CUt
 // ------------------------------------------------------------------ MMA issuer (warp 1)
 // Rows past the end of the sequence may hold any bits: zero them in the landed slot so
 // that a masked (zero) probability never meets a NaN or Inf in the value product.
-template <int kMode, bool kWin>
-__device__ __forceinline__ void prepare_slot(const Seg<kWin> &sg, int tile, uint32_t sbase, int n_valid, int lane) {
-  if constexpr (kWin) {
-    // also the rows before the window, which the cache may have lost
-    if (!sg.q.every_row(tile * kTile, kTile)) {
-      for (int idx = lane; idx < 2 * kTile * 8; idx += 32) {
-        const int at = idx / (kTile * 8), r = idx / 8 % kTile;
-        if (!sg.q.row(tile * kTile + r)) st_shared_v4(sbase + at * kAtomBytes + r * 128 + (idx % 8) * 16, 0u, 0u, 0u, 0u);
-      }
-      fence_proxy_async_smem();
-    }
-  } else if (kMode != kModeIndexed && n_valid < kTile) {
+template <int kMode>
+__device__ __forceinline__ void prepare_slot(uint32_t sbase, int n_valid, int lane) {
+  if (kMode != kModeIndexed && n_valid < kTile) {
     const int n_zero = (kTile - n_valid) * 8;  // 16-byte units per atom
     for (int idx = lane; idx < 2 * n_zero; idx += 32) {
       const int at = idx / n_zero, u = idx % n_zero;
@@ -406,7 +366,7 @@ __device__ __forceinline__ void prepare_slot(const Seg<kWin> &sg, int tile, uint
 // releases its ring slots).  MMAs of different threads are unordered, and the two streams
 // touch disjoint TMEM columns, so the pipe simply interleaves them.  Loop state and MMA
 // operands are warp-uniform; one elected lane issues.
-template <int kMode, bool kWin>
+template <int kMode>
 __device__ void score_mma_role(const AttendParams &p, const Shared &sh, uint32_t tmem, int iq, long long t0,
                                long long t1, int lane) {
   uint64_t *bar = sh.bar;
@@ -414,14 +374,14 @@ __device__ void score_mma_role(const AttendParams &p, const Shared &sh, uint32_t
   const uint32_t c_base = smem_u32(sh.slot(0));
   const uint32_t qt_base = smem_u32(sh.qt(0));
   uint32_t ns = 0, q_use = 0;
-  SegIter<kWin> it(t0, t1, iq);
-  Seg<kWin> sg;
+  SegIter it(t0, t1, iq);
+  Seg sg;
   while (it.next(p, kMode, sg)) {
     if (sg.empty) continue;
     if (!wait_warp(&bar[kBarQFull], q_use & 1, sh, p.status)) return;
     ++q_use;
-    for (int t = sg.lo; t < sg.hi; t = sg.next(t), ++ns) {
-      const int n_valid = min(kTile, sg.rows - sg.tile(t) * kTile);
+    for (int t = sg.lo; t < sg.hi; ++t, ++ns) {
+      const int n_valid = min(kTile, sg.rows - t * kTile);
       if (!wait_warp(&bar[kBarSEmpty + (ns & 1)], ((ns >> 1) & 1) ^ 1, sh, p.status)) return;
       const uint32_t d = tmem + kTmemS + (ns & 1) * kRows;
 #pragma unroll
@@ -430,7 +390,7 @@ __device__ void score_mma_role(const AttendParams &p, const Shared &sh, uint32_t
         const uint32_t k = ns * kSlotQuarters + sq;
         if (!wait_warp(&bar[kBarCFull + ring_pos(k)], ring_use(k) & 1, sh, p.status)) return;
         const uint32_t sbase = c_base + ring_pos(k) * kSlotBytes;
-        prepare_slot<kMode, kWin>(sg, sg.tile(t), sbase, n_valid, lane);
+        prepare_slot<kMode>(sbase, n_valid, lane);
         tc_fence_after();
         const uint64_t a0 = sw128_desc(sbase, 16, 1024);
         const uint64_t b0 = sw128_desc(qt_base + 2 * sq * kQtChunkBytes, 16, 1024);
@@ -448,14 +408,14 @@ __device__ void score_mma_role(const AttendParams &p, const Shared &sh, uint32_t
       }
       if (elect_one()) {
         umma_commit(&bar[kBarSFull + (ns & 1)]);
-        if (sg.next(t) >= sg.hi) umma_commit(&bar[kBarQEmpty]);
+        if (t == sg.hi - 1) umma_commit(&bar[kBarQEmpty]);
       }
       __syncwarp();
     }
   }
 }
 
-template <int kMode, bool kWin>
+template <int kMode>
 __device__ void value_mma_role(const AttendParams &p, const Shared &sh, uint32_t tmem, int iq, long long t0,
                                long long t1) {
   uint64_t *bar = sh.bar;
@@ -463,12 +423,12 @@ __device__ void value_mma_role(const AttendParams &p, const Shared &sh, uint32_t
   const uint32_t c_base = smem_u32(sh.slot(0));
   const uint32_t p_base = smem_u32(sh.pbuf(0));
   uint32_t no = 0, o_use = 0;
-  SegIter<kWin> it(t0, t1, iq);
-  Seg<kWin> sg;
+  SegIter it(t0, t1, iq);
+  Seg sg;
   while (it.next(p, kMode, sg)) {
     if (sg.empty) continue;
     if (!wait_warp(&bar[kBarOEmpty], (o_use & 1) ^ 1, sh, p.status)) return;
-    for (int t = sg.lo; t < sg.hi; t = sg.next(t), ++no) {
+    for (int t = sg.lo; t < sg.hi; ++t, ++no) {
       if (!wait_warp(&bar[kBarPFull + (no & 1)], (no >> 1) & 1, sh, p.status)) return;
       tc_fence_after();
       // O^T[latent, heads] += C_tile^T * P^T, four 128-lane latent blocks, K = 64 rows.
@@ -493,7 +453,7 @@ __device__ void value_mma_role(const AttendParams &p, const Shared &sh, uint32_t
           umma_commit(&bar[kBarCEmpty + rp[mb]]);
         }
         umma_commit(&bar[kBarPEmpty + (no & 1)]);
-        if (sg.next(t) >= sg.hi) umma_commit(&bar[kBarOFull]);
+        if (t == sg.hi - 1) umma_commit(&bar[kBarOFull]);
       }
       __syncwarp();
     }
@@ -512,7 +472,7 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
-template <int kMode, bool kWin>
+template <int kMode>
 __device__ void softmax_role(const AttendParams &p, const Shared &sh, uint32_t tmem, int g, int iq, long long t0,
                              long long t1, int warp, int lane) {
   uint64_t *bar = sh.bar;
@@ -531,8 +491,8 @@ __device__ void softmax_role(const AttendParams &p, const Shared &sh, uint32_t t
   uint32_t n = 0, o_use = 0;    // tiles seen by this CTA, segments finished
   if (tid < 32) m_used[col0 + tid] = -INFINITY;
   named_bar_sync(bar_id, 128);
-  SegIter<kWin> it(t0, t1, iq);
-  Seg<kWin> sg;
+  SegIter it(t0, t1, iq);
+  Seg sg;
   while (it.next(p, kMode, sg)) {
     if (sg.empty) {
       // no visible tile: an empty partial (weight zero in the merge)
@@ -565,7 +525,7 @@ __device__ void softmax_role(const AttendParams &p, const Shared &sh, uint32_t t
         if (k < p.K) ent_next[h2] = list[k];
       }
     }
-    for (int t = sg.lo; t < sg.hi; t = sg.next(t), ++n) {
+    for (int t = sg.lo; t < sg.hi; ++t, ++n) {
       const uint32_t sb = n & 1;
       int ent[2] = {ent_next[0], ent_next[1]};
       if constexpr (kMode == kModeIndexed) {
@@ -579,14 +539,7 @@ __device__ void softmax_role(const AttendParams &p, const Shared &sh, uint32_t t
       }
       mbar_wait(&bar[kBarSFull + sb], (n >> 1) & 1, sh.abort_flag, p.status);
       tc_fence_after();
-      bool v0, v1;
-      if constexpr (kWin) {
-        v0 = sg.q.row(sg.tile(t) * kTile + r0);
-        v1 = sg.q.row(sg.tile(t) * kTile + r0 + 8);
-      } else {
-        v0 = (t * kTile + r0) < n_vis;
-        v1 = (t * kTile + r0 + 8) < n_vis;
-      }
+      bool v0 = (t * kTile + r0) < n_vis, v1 = (t * kTile + r0 + 8) < n_vis;
       if constexpr (kMode == kModeIndexed) {
         v0 = v0 && ent[0] != kUnusedEntry;
         v1 = v1 && ent[1] != kUnusedEntry;
@@ -659,10 +612,8 @@ __device__ void softmax_role(const AttendParams &p, const Shared &sh, uint32_t t
           const float p0 = (x0 == -INFINITY) ? 0.f : fast_exp2(x0 - m_reg[2 * j]);
           const float p1 = (x1 == -INFINITY) ? 0.f : fast_exp2(x1 - m_reg[2 * j + 1]);
           const uint32_t w = pack_bf16x2(p0, p1);
-          // windows sum the unrounded values: lse is then exact to fp32 (o's error is the same,
-          // 2^-9 a weight either way)
-          l_part[2 * j] += kWin ? p0 : bf16lo_to_f32(w);
-          l_part[2 * j + 1] += kWin ? p1 : bf16hi_to_f32(w);
+          l_part[2 * j] += bf16lo_to_f32(w);
+          l_part[2 * j + 1] += bf16hi_to_f32(w);
           pw[2 * j + h] = w;
         }
       // this P buffer is free (the value product of tile n-2 has finished)
@@ -893,7 +844,7 @@ __device__ void cluster_merge(const AttendParams &p, const Shared &sh, int warp,
 }
 
 // ------------------------------------------------------------------ kernel
-template <int kMode, bool kWin>
+template <int kMode>
 // Bounds for 384 threads: eleven warps put three on some SM sub-partitions, whose 16K
 // registers then cap a thread at 168 (the 352-thread bound alone would allow 184).
 __global__ void __launch_bounds__(384, 1)
@@ -938,7 +889,7 @@ __global__ void __launch_bounds__(384, 1)
     tmem_relinquish();
   }
   grid_dep_launch();
-  if (kMode == kModeDense && !kWin && p.group_size == 1 && threadIdx.x == 0) {
+  if (kMode == kModeDense && p.group_size == 1 && threadIdx.x == 0) {
     // Decode (one query per sequence), while the previous kernel finishes: bring this
     // CTA's first two tiles into L2, at the place they would be if every sequence held
     // Lmax rows.  (A verify group's CTAs share their tiles; there the extra requests cost
@@ -957,9 +908,9 @@ __global__ void __launch_bounds__(384, 1)
   }
   grid_dep_wait();  // inputs (q~, lengths, tables, cache) may come from the previous kernel
   // tile range of this CTA's group
-  const long long T = warp_total_tiles<kWin>(p, kMode, lane);
+  const long long T = warp_total_tiles(p, kMode, lane);
   const long long G = p.groups;
-  if (blockIdx.x == 0 && warp == 0) warp_write_seq_prefix<kWin>(p, kMode, lane);
+  if (blockIdx.x == 0 && warp == 0) warp_write_seq_prefix(p, kMode, lane);
   const long long t0 = group_start(g, T, G), t1 = group_start(g + 1, T, G);
   tc_fence_before();
   __syncthreads();
@@ -971,15 +922,15 @@ __global__ void __launch_bounds__(384, 1)
       prefetch_tensormap(&tm_qt);
       if (kMode != kModeIndexed) prefetch_tensormap(&tm_cache);
     }
-    if (kMode == kModeIndexed || lane == 0) producer_role<kMode, kWin>(p, sh, &tm_cache, &tm_qt, iq, t0, t1, lane, 0);
+    if (kMode == kModeIndexed || lane == 0) producer_role<kMode>(p, sh, &tm_cache, &tm_qt, iq, t0, t1, lane, 0);
   } else if (warp == 11) {
-    if (kMode == kModeIndexed) producer_role<kMode, kWin>(p, sh, &tm_cache, &tm_qt, iq, t0, t1, lane, 1);
+    if (kMode == kModeIndexed) producer_role<kMode>(p, sh, &tm_cache, &tm_qt, iq, t0, t1, lane, 1);
   } else if (warp == 1) {
-    score_mma_role<kMode, kWin>(p, sh, tmem, iq, t0, t1, lane);
+    score_mma_role<kMode>(p, sh, tmem, iq, t0, t1, lane);
   } else if (warp == 10) {
-    value_mma_role<kMode, kWin>(p, sh, tmem, iq, t0, t1);
+    value_mma_role<kMode>(p, sh, tmem, iq, t0, t1);
   } else {
-    softmax_role<kMode, kWin>(p, sh, tmem, g, iq, t0, t1, warp, lane);
+    softmax_role<kMode>(p, sh, tmem, g, iq, t0, t1, warp, lane);
   }
 
   __syncwarp();
@@ -1178,11 +1129,11 @@ size_t attend_workspace_bytes_for(int B, int Q, int sms) {
          (size_t)B * (size_t)Q * (sizeof(long long) + sizeof(int32_t));
 }
 
-template <int kMode, bool kWin>
+template <int kMode>
 static cudaError_t launch_attend_mode(const CUtensorMap &tm_cache, const CUtensorMap &tm_qt, const AttendParams &p,
                                       cudaStream_t stream, bool with_combine) {
   static std::atomic<int> configured_device{-1};
-  const cudaError_t e0 = set_smem_limit_once(attend::attend_kernel<kMode, kWin>, attend::kSmemBytes, configured_device);
+  const cudaError_t e0 = set_smem_limit_once(attend::attend_kernel<kMode>, attend::kSmemBytes, configured_device);
   if (e0 != cudaSuccess) return e0;
   const int grid = p.groups * p.group_size;
   if (kMode == kModeIndexed && p.cluster > 0) {
@@ -1201,9 +1152,9 @@ static cudaError_t launch_attend_mode(const CUtensorMap &tm_cache, const CUtenso
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, attend::attend_kernel<kMode, kWin>, tm_cache, tm_qt, p);
+    return cudaLaunchKernelEx(&cfg, attend::attend_kernel<kMode>, tm_cache, tm_qt, p);
   }
-  cudaError_t e = launch_chained(attend::attend_kernel<kMode, kWin>, dim3(grid), dim3(attend::kThreads), attend::kSmemBytes,
+  cudaError_t e = launch_chained(attend::attend_kernel<kMode>, dim3(grid), dim3(attend::kThreads), attend::kSmemBytes,
                                  stream, tm_cache, tm_qt, p);
   if (e != cudaSuccess || !with_combine) return e;
   dim3 cgrid(p.B * p.Q, kHeads / attend::kCombineHeads);
@@ -1221,7 +1172,7 @@ int attend_indexed_cluster_capacity(int csize) {
   const auto it = cache.find({dev, csize});
   if (it != cache.end()) return it->second;
   int n = 0;
-  if (cudaFuncSetAttribute(attend::attend_kernel<kModeIndexed, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(attend::attend_kernel<kModeIndexed>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            attend::kSmemBytes) == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(csize);
@@ -1234,7 +1185,7 @@ int attend_indexed_cluster_capacity(int csize) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, attend::attend_kernel<kModeIndexed, false>, &cfg) != cudaSuccess) n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, attend::attend_kernel<kModeIndexed>, &cfg) != cudaSuccess) n = 0;
   }
   cudaGetLastError();  // a failed query is not an error of the caller's: the combine path runs
   cache[{dev, csize}] = n;
@@ -1245,13 +1196,11 @@ cudaError_t launch_attend(int mode, const CUtensorMap &tm_cache, const CUtensorM
                           cudaStream_t stream, bool with_combine) {
   switch (mode) {
     case kModeDense:
-      return p.window > 0 ? launch_attend_mode<kModeDense, true>(tm_cache, tm_qt, p, stream, with_combine)
-                          : launch_attend_mode<kModeDense, false>(tm_cache, tm_qt, p, stream, with_combine);
+      return launch_attend_mode<kModeDense>(tm_cache, tm_qt, p, stream, with_combine);
     case kModePaged:
-      return p.window > 0 ? launch_attend_mode<kModePaged, true>(tm_cache, tm_qt, p, stream, with_combine)
-                          : launch_attend_mode<kModePaged, false>(tm_cache, tm_qt, p, stream, with_combine);
+      return launch_attend_mode<kModePaged>(tm_cache, tm_qt, p, stream, with_combine);
     default:
-      return launch_attend_mode<kModeIndexed, false>(tm_cache, tm_qt, p, stream, with_combine);
+      return launch_attend_mode<kModeIndexed>(tm_cache, tm_qt, p, stream, with_combine);
   }
 }
 

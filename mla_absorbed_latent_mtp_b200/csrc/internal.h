@@ -32,7 +32,6 @@ struct AttendParams {
   int cluster;                // indexed: CTAs per list, launched as one thread-block cluster that
                               // merges its partials in distributed shared memory and writes
                               // o_latent / lse itself (no combine); 0: partials to the workspace
-  int window, sinks;          // dense/paged: sliding window (0: none) and rows that stay visible
   float scale_log2;           // softmax scale * log2(e)
   float *part_o;              // [slots, H, R] unnormalised partial outputs
   float *part_m;              // [slots, H] running max (log2 units)

@@ -158,7 +158,7 @@ __device__ __forceinline__ int seq_len(const AttendPackedParams &p, int b) {
   return min(max(p.a.seq_lens[b], 0), p.a.max_pages * kPageTokens);
 }
 __device__ __forceinline__ int seq_tiles(const AttendPackedParams &p, int L) {
-  return SeqTiles(L, p.a.Q, p.a.window, p.a.sinks).count;
+  return SeqTiles(L, p.a.Q, p.window, p.sinks).count;
 }
 
 // floor(g T / G), in 32 bits where the list allows it.
@@ -249,7 +249,7 @@ struct SegIter {
       nt = seq_tiles(p, L);
     }
     sg.b = s;
-    sg.q = QueryTiles(L, p.a.Q, iq, p.a.window, p.a.sinks);
+    sg.q = QueryTiles(L, p.a.Q, iq, p.window, p.sinks);
     sg.lo = (int)(t - base);
     const long long end = min(t_end - base, (long long)nt);
     sg.hi = min((int)end, sg.q.e);

@@ -6,8 +6,9 @@
 namespace mla {
 
 struct AttendPackedParams {
-  AttendParams a;             // sizes, seq_lens, page_table, window and sinks, workspace parts, outputs, status
+  AttendParams a;             // sizes, seq_lens, page_table, workspace parts, outputs, status
   const uint16_t *q_tilde;    // [B, Q, H, R]
+  int window, sinks;          // window 0: every row up to the query's own
   float unit;                 // c = unit * scale * code
   float score_factor;         // softmax scale * log2(e) * unit
 };
