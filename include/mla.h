@@ -315,7 +315,8 @@ mla_status mla_attend_packed(const uint16_t *q_tilde, const uint8_t *pool, const
  * The calls keep refs in step with page_table, and expect it so.  Free pages are taken lowest first, by
  * sequence (fork: by list entry) and then by position; the results do not depend on timing.
  * workspace: mla_pages_workspace_bytes(n, num_pages), n = B (reserve), n forks, 1 (compact); it
- * holds nothing between calls.  The pages describe no allocator.
+ * holds nothing between calls, and calls that may run at the same time need one each (and must not
+ * share the state either: they are not atomic against each other).  The pages describe no allocator.
  *
  * mla_pages_reserve: gives every sequence room for Q more rows (before mla_cache_append_*): maps its
  *   unmapped pages among those of positions L_b .. L_b + Q - 1, and replaces a page among them that

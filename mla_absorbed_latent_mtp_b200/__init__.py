@@ -164,6 +164,14 @@ def _check_current(*tensors):
         raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{_torch.cuda.current_device()}")
 
 
+def _used_on(stream, *tensors):
+    """Tells torch's allocator that tensors made here are used on the `stream` of the call."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _require(t, name, dtype, shape=None, min_numel=None, optional=False):
     """Refuse, before any pointer reaches the C ABI, a tensor whose dtype, layout or size
     would let a kernel read or write outside it: the kernels address memory only from the
@@ -341,6 +349,7 @@ def mla_attend_window_dense(q_tilde, cache, window, sinks=0, seq_lens=None, scal
     _check_current(q_tilde, cache, seq_lens, workspace, o_latent, lse, status)
     workspace = new_workspace(B, Q) if workspace is None else workspace
     o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
+    _used_on(stream, workspace, o_latent, lse)
     _check("mla_attend_window_dense", lib().mla_attend_window_dense(
         _ptr(q_tilde), _ptr(cache), _ptr(seq_lens), B, Q, H, R, cache.shape[1], scale, window, sinks, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _ptr(o_latent), _ptr(lse), _ptr(status), _stream(stream)))
@@ -358,6 +367,7 @@ def mla_attend_window_paged(q_tilde, pool, page_table, seq_lens, window, sinks=0
     _check_current(q_tilde, pool, page_table, seq_lens, workspace, o_latent, lse, status)
     workspace = new_workspace(B, Q) if workspace is None else workspace
     o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
+    _used_on(stream, workspace, o_latent, lse)
     _check("mla_attend_window_paged", lib().mla_attend_window_paged(
         _ptr(q_tilde), _ptr(pool), _ptr(page_table), _ptr(seq_lens), B, Q, H, R, pool.shape[1], page_table.shape[1],
         pool.shape[0], scale, window, sinks, _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -594,6 +604,7 @@ def mla_cache_unpack(pool, page_table, start, n, unit=1.0, rows=None, status=Non
     _check_current(pool, page_table, start, rows, status)
     if rows is None:
         rows = torch.empty(B, n, R, dtype=torch.bfloat16, device=pool.device)
+    _used_on(stream, rows)
     _check("mla_cache_unpack", lib().mla_cache_unpack(
         _ptr(pool), _ptr(page_table), _ptr(start), _ptr(rows), B, n, R, PAGE, page_table.shape[1], pool.shape[0],
         unit, _ptr(status), _stream(stream)))
@@ -609,6 +620,7 @@ def mla_attend_packed(q_tilde, pool, page_table, seq_lens, unit=1.0, window=0, s
     _check_current(q_tilde, pool, page_table, seq_lens, workspace, o_latent, lse, status)
     workspace = new_workspace(B, Q) if workspace is None else workspace
     o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
+    _used_on(stream, workspace, o_latent, lse)
     _check("mla_attend_packed", lib().mla_attend_packed(
         _ptr(q_tilde), _ptr(pool), _ptr(page_table), _ptr(seq_lens), B, Q, H, R, PAGE, page_table.shape[1],
         pool.shape[0], unit, window, sinks, scale, _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -652,6 +664,7 @@ def mla_pages_reserve(pool, page_table, seq_lens, refs, q_len, workspace=None, s
     page_bytes = _check_page_pool(pool, refs, B, workspace)
     _check_current(pool, page_table, seq_lens, refs, workspace, status)
     workspace = new_pages_workspace(B, pool.shape[0]) if workspace is None else workspace
+    _used_on(stream, workspace)
     _check("mla_pages_reserve", lib().mla_pages_reserve(
         _ptr(pool), page_bytes, _ptr(page_table), _ptr(seq_lens), _ptr(refs), B, q_len, max_pages, pool.shape[0],
         _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
@@ -667,6 +680,7 @@ def mla_pages_fork(pool, page_table, seq_lens, refs, parents, children, workspac
     page_bytes = _check_page_pool(pool, refs, n, workspace)
     _check_current(pool, page_table, seq_lens, refs, parents, children, workspace, status)
     workspace = new_pages_workspace(n, pool.shape[0]) if workspace is None else workspace
+    _used_on(stream, workspace)
     _check("mla_pages_fork", lib().mla_pages_fork(
         _ptr(pool), page_bytes, _ptr(page_table), _ptr(seq_lens), _ptr(refs), _ptr(parents), _ptr(children), n, B,
         max_pages, pool.shape[0], _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
@@ -691,6 +705,7 @@ def mla_pages_compact(pool, page_table, refs, n_used=None, workspace=None, statu
     if n_used is None:
         n_used = torch.empty(1, dtype=torch.int32, device=pool.device)
     workspace = new_pages_workspace(1, pool.shape[0]) if workspace is None else workspace
+    _used_on(stream, workspace, n_used)
     _check("mla_pages_compact", lib().mla_pages_compact(
         _ptr(pool), page_bytes, _ptr(page_table), _ptr(refs), page_table.shape[0], page_table.shape[1], pool.shape[0],
         _ptr(n_used), _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))

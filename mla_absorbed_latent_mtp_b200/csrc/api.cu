@@ -197,7 +197,10 @@ static mla_status attend_common(int mode, const uint16_t *q_tilde, const uint16_
   p.lse = lse;
   p.status = status;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (window > 0) return cuda_status(launch_attend_window(mode == kModePaged, tm_cache, tm_qt, p, st));
+  if (window > 0) {
+    p.groups = std::min(p.groups, 256);  // a sequence has at most one partial per group
+    return cuda_status(launch_attend_window(mode == kModePaged, tm_cache, tm_qt, p, st));
+  }
   if (!fused) return cuda_status(launch_attend(mode, tm_cache, tm_qt, p, st));
   CUtensorMap tm_w;
   if (!make_w_uv_map(&tm_w, w_uv)) return cuda_status(cudaErrorInvalidValue);
@@ -238,24 +241,24 @@ static mla_status attend_packed_common(const uint16_t *q_tilde, const uint8_t *p
       return cuda_status(cudaErrorInvalidValue);
   }
   AttendPackedParams p = {};
-  p.a.seq_lens = seq_lens;
-  p.a.page_table = page_table;
-  p.a.B = B;
-  p.a.Q = Q;
-  p.a.Lmax = max_pages * kPageTokens;
-  p.a.max_pages = max_pages;
-  p.a.num_pages = num_pages;
-  p.a.group_size = Q;
-  p.a.groups = std::max(1, sms / Q);
+  p.seq_lens = seq_lens;
+  p.page_table = page_table;
+  p.B = B;
+  p.Q = Q;
+  p.Lmax = max_pages * kPageTokens;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.group_size = Q;
+  p.groups = std::min(std::max(1, sms / Q), 256);  // a sequence has at most one partial per group
   const size_t slots = attend_slots(B, Q, sms);
-  p.a.part_o = reinterpret_cast<float *>(workspace);
-  p.a.part_m = p.a.part_o + slots * kHeads * kLatent;
-  p.a.part_l = p.a.part_m + slots * kHeads;
-  p.a.seq_ts = reinterpret_cast<long long *>(p.a.part_l + slots * kHeads);
-  p.a.seq_nt = reinterpret_cast<int32_t *>(p.a.seq_ts + (size_t)B * Q);
-  p.a.o_latent = o_latent;
-  p.a.lse = lse;
-  p.a.status = status;
+  p.part_o = reinterpret_cast<float *>(workspace);
+  p.part_m = p.part_o + slots * kHeads * kLatent;
+  p.part_l = p.part_m + slots * kHeads;
+  p.seq_ts = reinterpret_cast<long long *>(p.part_l + slots * kHeads);
+  p.seq_nt = reinterpret_cast<int32_t *>(p.seq_ts + (size_t)B * Q);
+  p.o_latent = o_latent;
+  p.lse = lse;
+  p.status = status;
   p.q_tilde = q_tilde;
   p.window = window;
   p.sinks = sinks;

@@ -1,0 +1,323 @@
+// lists.cuh -- the tile list of a windowed or packed attention: which range of it a CTA group takes,
+// where the partials are, and the kernels that merge them.
+//
+// The list holds, sequence after sequence, the tiles that its queries may see (window.cuh), and G
+// groups take equal ranges of it.  `Seqs` gives a kernel's lengths and tile counts:
+//   length(p, b)      rows of sequence b, clamped to the cache;  bad_length(p, b): it was clamped
+//   tiles(p, L)       list tiles of a sequence of L rows
+#pragma once
+
+#include <math.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "sm100.cuh"
+#include "split.cuh"
+
+namespace mla {
+namespace lists {
+
+// A CTA group's range of the list, and the sequence that holds its first tile.
+struct Range {
+  long long t0, t1, base;  // base: first tile of sequence s
+  int s, L, start;         // its length, and the list's start places per sequence
+};
+
+// Places of a sequence in the list: its tiles, and before them `start` places without work, which
+// stand for what a CTA pays when it begins another sequence (an empty pipeline, q~, the last
+// one's partial), so that ranges of equal length are equal in time: Seqs::kStart, fewer where a
+// CTA has hardly any tiles, and none where it has at most one.  (4-bit rows, tiles of 128, kStart 3:
+// 32 x 8,192 rows 75.2 us without, 67.9 with; 32 x 1,024: 35.9 without, 25.6 with one place, 28.9
+// with three; 32 x 512: 22.9 without, 25.7 with three.  bf16 windows, tiles of 64: 32 x (4,096 + 64)
+// 43.5 us without, 41.7 / 42.7 / 42.8 with 3 / 5 / 8; 16 x 6 queries, window 4,095: 93.9, 89.5 / 88.9 / 92.5.)
+template <class Seqs>
+__device__ __forceinline__ int start_places(long long tiles, int seqs, int G) {
+  return tiles <= G ? 0 : (tiles >= 2LL * G && tiles >= 8LL * seqs) ? Seqs::kStart : 1;
+}
+template <class Seqs, class P>
+__device__ __forceinline__ int places(const P &p, int L, int start) {
+  const int n = Seqs::tiles(p, L);
+  return n > 0 ? n + start : 0;
+}
+
+__device__ __forceinline__ int warp_scan(int x, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// The list's length and its start places, by one warp.
+template <class Seqs, class P>
+__device__ long long list_length(const P &p, int lane, int &start) {
+  long long tiles = 0;
+  int seqs = 0;
+  for (int s0 = 0; s0 < p.B; s0 += 32) {
+    const int n = s0 + lane < p.B ? Seqs::tiles(p, Seqs::length(p, s0 + lane)) : 0;
+    tiles += __reduce_add_sync(0xffffffffu, n);
+    seqs += __popc(__ballot_sync(0xffffffffu, n > 0));
+  }
+  start = start_places<Seqs>(tiles, seqs, p.groups);
+  return tiles + (long long)start * seqs;
+}
+
+// floor(g T / G), in 32 bits where the list allows it.
+__device__ __forceinline__ long long group_start(int g, long long T, int G) {
+  if (T >= (1LL << 31)) return split::group_start(g, T, G);
+  const uint32_t q = (uint32_t)T / (uint32_t)G, r = (uint32_t)T % (uint32_t)G;
+  return (long long)g * q + (uint32_t)g * r / (uint32_t)G;  // G is at most the number of SMs
+}
+
+// By one warp, with scans in steps of 32 sequences (a walk from the first sequence cost the last
+// CTAs of a 32-sequence step a microsecond).
+template <class Seqs, class P>
+__device__ Range find_range(const P &p, int g, int lane) {
+  Range r = {0, 0, 0, 0, 0, 0};
+  const long long T = list_length<Seqs>(p, lane, r.start);
+  r.t0 = group_start(g, T, p.groups);
+  r.t1 = group_start(g + 1, T, p.groups);
+  if (r.t0 >= r.t1) return r;
+  for (int s0 = 0; s0 < p.B; s0 += 32) {
+    const int L = s0 + lane < p.B ? Seqs::length(p, s0 + lane) : 0;
+    const int n = s0 + lane < p.B ? places<Seqs>(p, L, r.start) : 0;
+    const int x = warp_scan(n, lane);
+    const uint32_t behind = __ballot_sync(0xffffffffu, r.base + x > r.t0);  // the range starts before their end
+    if (behind) {
+      const int l = __ffs(behind) - 1;
+      r.s = s0 + l;
+      r.L = __shfl_sync(0xffffffffu, L, l);
+      r.base += __shfl_sync(0xffffffffu, x - n, l);
+      break;
+    }
+    r.base += __shfl_sync(0xffffffffu, x, 31);
+  }
+  return r;
+}
+
+// Where each sequence's partials are, for the combine: with at least as many places as groups they
+// are those of `count` consecutive groups, seq_ts = count << 32 | first group; with fewer every
+// place is a group of its own, seq_ts = -1 - first place, seq_nt places of T (written as the last
+// sequence's end).
+template <class Seqs, class P>
+__device__ void write_partial_table(const P &p, int lane) {
+  int start;
+  const long long T = list_length<Seqs>(p, lane, start);
+  const long long G = p.groups;
+  long long base = 0;
+  for (int s0 = 0; s0 < p.B; s0 += 32) {
+    const int s = s0 + lane;
+    const int n = s < p.B ? places<Seqs>(p, Seqs::length(p, s), start) : 0;
+    const int x = warp_scan(n, lane);
+    if (s < p.B) {
+      const long long ts = base + x - n;
+      p.seq_nt[s] = n;
+      if (T < G) {
+        p.seq_ts[s] = -1 - ts;
+      } else if (n == 0) {
+        p.seq_ts[s] = 0;
+      } else {
+        const long long first = split::group_of(ts, T, G), last = split::group_of(ts + n - 1, T, G);
+        p.seq_ts[s] = (last - first + 1) << 32 | first;
+      }
+    }
+    base += __shfl_sync(0xffffffffu, x, 31);
+  }
+}
+
+// ------------------------------------------------------------------ combine
+// Merges the partials of a query row: with M the largest running max and w_k = 2^(m_k - M),
+// o = unit * sum w_k O_k / sum w_k l_k and lse = (M + log2 sum w_k l_k) ln 2.  Thread t of 128 loads
+// values 4t .. 4t + 3 of a partial, in the order that the attend kernel found convenient; the row
+// goes through shared memory to its latents' places, Order::latent.
+//
+// The places of sequence b's partials, from write_partial_table.
+struct Partials {
+  int count, first, ts, T;
+  template <class P>
+  __device__ __forceinline__ Partials(const P &p, int b) : first(0), ts(-1), T(0) {
+    const long long place = p.seq_ts[b];
+    if (place < 0) {  // fewer places than groups
+      count = p.seq_nt[b];
+      ts = (int)(-1 - place);
+      T = (int)(-1 - p.seq_ts[p.B - 1]) + p.seq_nt[p.B - 1];
+    } else {
+      count = (int)(place >> 32);
+      first = (int)place;
+    }
+  }
+  template <class P>
+  __device__ __forceinline__ long long slot(const P &p, int k, int b, int i) const {
+    const int g = ts >= 0 ? ((ts + k + 1) * p.groups - 1) / T : first + k;
+    return split::partial_slot(p, kModePaged, g, b, i);
+  }
+};
+
+template <class Seqs, class P>
+__device__ __forceinline__ void report_length(const P &p, int b) {
+  if (Seqs::bad_length(p, b)) report_status(p.status, kStatusIndex);
+}
+
+template <class Order>
+__device__ __forceinline__ void row_to_shared(uint16_t *row, const float4 &o, float inv, int t) {
+  const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) row[Order::latent(4 * t + e)] = (uint16_t)(pack_bf16x2(v[e], 0.f) & 0xFFFFu);
+}
+template <class P>
+__device__ __forceinline__ void write_row(const P &p, long long at, const uint16_t *row, float M,
+                                          float den, int t) {
+  reinterpret_cast<uint2 *>(p.o_latent + at * kLatent)[t] = reinterpret_cast<const uint2 *>(row)[t];
+  if (p.lse != nullptr && t == 0)
+    p.lse[at] = M == -INFINITY ? -INFINITY : (M + log2f(den)) * 0.69314718055994530942f;
+}
+
+// Many query rows, few partials each: a block takes two heads of a row and merges online, three
+// partials at a time, all their loads in flight at once.
+constexpr int kFewHeads = 2, kFewChunk = 3;
+template <class Seqs, class Order, class P>
+__global__ void __launch_bounds__(128, 8) combine_few_kernel(const P p, float unit) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int v = blockIdx.x, b = v / p.Q, i = v % p.Q, t = threadIdx.x;
+  const int h0 = blockIdx.y * kFewHeads;
+  __shared__ __align__(16) uint16_t row[kFewHeads][kLatent];
+  const Partials pt(p, b);
+  if (t == 0 && blockIdx.y == 0 && i == 0) report_length<Seqs>(p, b);
+  float M[kFewHeads], den[kFewHeads];
+  float4 acc[kFewHeads];
+#pragma unroll
+  for (int hh = 0; hh < kFewHeads; ++hh) {
+    M[hh] = -INFINITY;
+    den[hh] = 0.f;
+    acc[hh] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int k0 = 0; k0 < pt.count; k0 += kFewChunk) {
+    float mk[kFewHeads][kFewChunk], lk[kFewHeads][kFewChunk];
+    float4 ok[kFewHeads][kFewChunk];
+#pragma unroll
+    for (int j = 0; j < kFewChunk; ++j) {
+      const bool live = k0 + j < pt.count;
+      const long long slot = live ? pt.slot(p, k0 + j, b, i) : 0;
+#pragma unroll
+      for (int hh = 0; hh < kFewHeads; ++hh) {
+        const long long r = slot * kHeads + h0 + hh;
+        mk[hh][j] = live ? p.part_m[r] : -INFINITY;
+        lk[hh][j] = live ? p.part_l[r] : 0.f;
+        ok[hh][j] = live ? *reinterpret_cast<const float4 *>(p.part_o + r * kLatent + 4 * t)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+#pragma unroll
+    for (int hh = 0; hh < kFewHeads; ++hh) {
+      float mx = M[hh];
+#pragma unroll
+      for (int j = 0; j < kFewChunk; ++j) mx = fmaxf(mx, mk[hh][j]);
+      if (mx == -INFINITY) continue;
+      const float a = exp2f(M[hh] - mx);  // 0 when M was -inf
+      den[hh] *= a;
+      acc[hh].x *= a;
+      acc[hh].y *= a;
+      acc[hh].z *= a;
+      acc[hh].w *= a;
+#pragma unroll
+      for (int j = 0; j < kFewChunk; ++j) {
+        if (mk[hh][j] == -INFINITY) continue;  // an empty partial's O was never written
+        const float w = exp2f(mk[hh][j] - mx);
+        den[hh] += w * lk[hh][j];
+        acc[hh].x += w * ok[hh][j].x;
+        acc[hh].y += w * ok[hh][j].y;
+        acc[hh].z += w * ok[hh][j].z;
+        acc[hh].w += w * ok[hh][j].w;
+      }
+      M[hh] = mx;
+    }
+  }
+#pragma unroll
+  for (int hh = 0; hh < kFewHeads; ++hh)
+    row_to_shared<Order>(row[hh], acc[hh], M[hh] == -INFINITY ? 0.f : unit / den[hh], t);
+  __syncthreads();
+#pragma unroll
+  for (int hh = 0; hh < kFewHeads; ++hh) write_row(p, (long long)v * kHeads + h0 + hh, row[hh], M[hh], den[hh], t);
+}
+
+// Few sequences, many partials each: a block takes one head of a row; eight slices of 128 threads
+// take every eighth partial, all of a thread's loads independent, and are added up in order (1 x
+// 8,192 rows, 64 partials: the call 66.6 us with the kernel above, 22.4 with this one).
+constexpr int kSlices = 8;
+constexpr int kMaxPartials = 256;  // per sequence: at most one per CTA group
+template <class Seqs, class Order, class P>
+__global__ void __launch_bounds__(128 * kSlices) combine_many_kernel(const P p, float unit) {
+  grid_dep_launch();
+  grid_dep_wait();
+  const int v = blockIdx.x, b = v / p.Q, i = v % p.Q, h = blockIdx.y;
+  const int t = threadIdx.x % 128, slice = threadIdx.x / 128, lane = threadIdx.x % 32;
+  __shared__ long long slots[kMaxPartials];
+  __shared__ float weight[kMaxPartials];
+  __shared__ float4 sum[kSlices][128];
+  __shared__ __align__(16) uint16_t row[kLatent];
+  __shared__ float total, top;
+  const Partials pt(p, b);
+  if (threadIdx.x == 0 && h == 0 && i == 0) report_length<Seqs>(p, b);
+  if (threadIdx.x < 32) {
+    float M = -INFINITY, den = 0.f;
+    for (int k = lane; k < pt.count; k += 32) {
+      slots[k] = pt.slot(p, k, b, i);
+      weight[k] = p.part_m[slots[k] * kHeads + h];
+      M = fmaxf(M, weight[k]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int k = lane; k < pt.count; k += 32) {
+      const float w = weight[k] == -INFINITY ? 0.f : exp2f(weight[k] - M);  // an empty partial's O was never written
+      weight[k] = w;
+      if (w != 0.f) den += w * p.part_l[slots[k] * kHeads + h];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    if (lane == 0) {
+      total = den;
+      top = M;
+    }
+  }
+  __syncthreads();
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = slice; k < pt.count; k += kSlices) {
+    const float w = weight[k];
+    const float *at = p.part_o + (slots[k] * kHeads + h) * kLatent + 4 * t;
+    const float4 o = w != 0.f ? *reinterpret_cast<const float4 *>(at) : make_float4(0.f, 0.f, 0.f, 0.f);
+    acc.x += w * o.x;
+    acc.y += w * o.y;
+    acc.z += w * o.z;
+    acc.w += w * o.w;
+  }
+  sum[slice][t] = acc;
+  __syncthreads();
+  if (slice == 0) {
+    for (int s = 1; s < kSlices; ++s) {
+      const float4 o = sum[s][t];
+      acc.x += o.x;
+      acc.y += o.y;
+      acc.z += o.z;
+      acc.w += o.w;
+    }
+    row_to_shared<Order>(row, acc, top == -INFINITY ? 0.f : unit / total, t);
+  }
+  __syncthreads();
+  if (slice == 0) write_row(p, (long long)v * kHeads + h, row, top, total, t);
+}
+
+template <class Seqs, class Order, class P>
+cudaError_t launch_combine(const P &p, float unit, cudaStream_t stream) {
+  if (p.B <= p.groups / 16)  // sixteen partials a sequence or more
+    return launch_chained(combine_many_kernel<Seqs, Order, P>, dim3(p.B * p.Q, kHeads), dim3(128 * kSlices), 0, stream,
+                          p, unit);
+  return launch_chained(combine_few_kernel<Seqs, Order, P>, dim3(p.B * p.Q, kHeads / kFewHeads), dim3(128), 0, stream,
+                        p, unit);
+}
+
+}  // namespace lists
+}  // namespace mla

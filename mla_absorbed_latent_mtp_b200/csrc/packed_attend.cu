@@ -18,7 +18,7 @@
 // reads the eight bytes of one scale group (16 latents) of four rows, interleaves the nibbles
 // of two rows so that one conversion yields the pair (row, row + 1) of a latent, and stores
 // its 4 x 4 block by a 16x256b tensor-memory store; which latent lands on which lane is free,
-// since O^T's lanes only have to be read back the same way (out_latent).
+// since O^T's lanes only have to be read back the same way (PartialOrder).
 //
 // Operands are fp16: code * scale is exact there.  q~ (bf16) is converted once per segment with
 // a power of two per head that puts the head's largest value in [2^14, 2^15): exact unless a
@@ -34,6 +34,7 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "lists.cuh"
 #include "packed.cuh"
 #include "packed_attend.h"
 #include "sm100.cuh"
@@ -58,12 +59,6 @@ constexpr int kSoftmaxWarps = 8;
 constexpr float kTau = 8.f;                     // the running max is raised when a score exceeds it by this
 constexpr float kShift = 7.f;                   // P is stored as 2^7 p
 
-// A CTA's range of the tile list, and the sequence that holds its first tile.
-struct Range {
-  long long t0, t1, base;  // base: first tile of sequence s
-  int s, L;                // and its length
-};
-
 constexpr int kOffQ = kRawSlots * kRawBytes;
 constexpr int kOffP = kOffQ + 8 * kQChunkBytes;
 constexpr int kOffRed = kOffP + 2 * kPBytes;    // [4][64] floats
@@ -80,7 +75,7 @@ constexpr int kBarRawFull = 0, kBarRawEmpty = kBarRawFull + kRawSlots, kBarSAFul
               kNumBars = kBarDrain + 1;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
 constexpr int kOffRange = kOffMisc + 16;
-constexpr int kSmemBytes = kOffRange + (int)sizeof(Range) + 1024;  // slack for 1024-byte alignment of the base
+constexpr int kSmemBytes = kOffRange + (int)sizeof(lists::Range) + 1024;  // slack for 1024-byte alignment of the base
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 // Tensor memory columns.
@@ -91,11 +86,13 @@ using SeqTiles = window::SeqTiles<kTile>;
 using QueryTiles = window::QueryTiles<kTile>;
 
 // Lane L of block mb of O^T holds latent 16 (8 (L / 32) + L % 8) + 4 mb + (L % 32) / 8; a
-// partial is stored in (block, lane) order.  The partial index of latent `lat`:
-__device__ __forceinline__ int partial_index(int lat) {
-  const int grp = lat / kGroup, nib = lat % kGroup;
-  return (nib >> 2) * 128 + (grp >> 3) * 32 + (nib & 3) * 8 + (grp & 7);
-}
+// partial is stored in (block, lane) order.
+struct PartialOrder {
+  static __device__ __forceinline__ int latent(int idx) {
+    const int mb = idx / 128, L = idx % 128;
+    return kGroup * (8 * (L / 32) + L % 8) + 4 * mb + L % 32 / 8;
+  }
+};
 
 // Instruction descriptor, kind::f16 with fp16 A and B and fp32 D.
 constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
@@ -140,7 +137,8 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 
 // Pairs of floats in one instruction: d = a b + c, d += a.
-__device__ __forceinline__ void fma_f32x2(float &d0, float &d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+__device__ __forceinline__ void fma_f32x2(float &d0, float &d1, float a0, float a1, float b0, float b1, float c0,
+                                          float c1) {
   asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
       "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
       : "=f"(d0), "=f"(d1)
@@ -154,76 +152,19 @@ __device__ __forceinline__ void add_f32x2(float &d0, float &d1, float a0, float 
 }
 
 // ------------------------------------------------------------------ the tile list
-__device__ __forceinline__ int seq_len(const AttendPackedParams &p, int b) {
-  return min(max(p.a.seq_lens[b], 0), p.a.max_pages * kPageTokens);
-}
-__device__ __forceinline__ int seq_tiles(const AttendPackedParams &p, int L) {
-  return SeqTiles(L, p.a.Q, p.window, p.sinks).count;
-}
-
-// floor(g T / G), in 32 bits where the list allows it.
-__device__ __forceinline__ long long group_start(int g, long long T, int G) {
-  if (T >= (1LL << 31)) return split::group_start(g, T, G);
-  const uint32_t q = (uint32_t)T / (uint32_t)G, r = (uint32_t)T % (uint32_t)G;
-  return (long long)g * q + (uint32_t)g * r / (uint32_t)G;  // G is at most the number of SMs
-}
-
-// By one warp, with an inclusive scan in steps of 32 sequences (a walk from the first sequence cost
-// the last CTAs of a 32-sequence step a microsecond).
-__device__ Range find_range(const AttendPackedParams &p, int g, int lane) {
-  int L = 0;
-  auto scan = [&](int s0, int &nt) {
-    L = s0 + lane < p.a.B ? seq_len(p, s0 + lane) : 0;
-    nt = s0 + lane < p.a.B ? seq_tiles(p, L) : 0;
-    int x = nt;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    return x;
-  };
-  long long T = 0;
-  int nt, x = 0;
-  for (int s0 = 0; s0 < p.a.B; s0 += 32) {
-    x = scan(s0, nt);
-    T += __shfl_sync(0xffffffffu, x, 31);
+struct Seqs {  // for lists.cuh
+  static constexpr int kStart = 3;
+  static __device__ __forceinline__ int length(const AttendPackedParams &p, int b) {
+    return min(max(p.seq_lens[b], 0), p.max_pages * kPageTokens);
   }
-  Range r = {group_start(g, T, p.a.groups), group_start(g + 1, T, p.a.groups), 0, 0, 0};
-  if (r.t0 >= r.t1) return r;
-  for (int s0 = 0; s0 < p.a.B; s0 += 32) {
-    if (p.a.B > 32) x = scan(s0, nt);
-    const uint32_t behind = __ballot_sync(0xffffffffu, r.base + x > r.t0);  // the range starts before their end
-    if (behind) {
-      const int l = __ffs(behind) - 1;
-      r.s = s0 + l;
-      r.L = __shfl_sync(0xffffffffu, L, l);
-      r.base += __shfl_sync(0xffffffffu, x - nt, l);
-      break;
-    }
-    r.base += __shfl_sync(0xffffffffu, x, 31);
+  static __device__ __forceinline__ int tiles(const AttendPackedParams &p, int L) {
+    return SeqTiles(L, p.Q, p.window, p.sinks).count;
   }
-  return r;
-}
-
-__device__ void warp_write_seq_prefix(const AttendPackedParams &p, int lane) {
-  long long base = 0;
-  for (int s0 = 0; s0 < p.a.B; s0 += 32) {
-    const int s = s0 + lane;
-    const int nt = s < p.a.B ? seq_tiles(p, seq_len(p, s)) : 0;
-    long long x = nt;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (s < p.a.B) {
-      p.a.seq_ts[s] = base + x - nt;
-      p.a.seq_nt[s] = nt;
-    }
-    base += __shfl_sync(0xffffffffu, x, 31);
+  static __device__ __forceinline__ bool bad_length(const AttendPackedParams &p, int b) {
+    return p.seq_lens[b] < 0 || p.seq_lens[b] > p.max_pages * kPageTokens;
   }
-}
+};
+using lists::Range;
 
 // Walks the segments (the pieces of sequences) of the list range [t, t_end).  A segment's tiles
 // for this CTA's query are n = first(), then next(n), below hi; none: its partial is empty.
@@ -238,21 +179,22 @@ struct Segment {
 };
 struct SegIter {
   long long t, t_end, base;
-  int s, L, iq;
-  __device__ SegIter(const Range &r, int iq_) : t(r.t0), t_end(r.t1), base(r.base), s(r.s), L(r.L), iq(iq_) {}
+  int s, L, start, iq;
+  __device__ SegIter(const Range &r, int iq_)
+      : t(r.t0), t_end(r.t1), base(r.base), s(r.s), L(r.L), start(r.start), iq(iq_) {}
   __device__ bool next(const AttendPackedParams &p, Segment &sg) {
     if (t >= t_end) return false;
-    int nt = seq_tiles(p, L);
-    while (base + nt <= t) {
-      base += nt;
-      L = seq_len(p, ++s);
-      nt = seq_tiles(p, L);
+    int n = lists::places<Seqs>(p, L, start);
+    while (base + n <= t) {
+      base += n;
+      L = Seqs::length(p, ++s);
+      n = lists::places<Seqs>(p, L, start);
     }
     sg.b = s;
-    sg.q = QueryTiles(L, p.a.Q, iq, p.window, p.sinks);
-    sg.lo = (int)(t - base);
-    const long long end = min(t_end - base, (long long)nt);
-    sg.hi = min((int)end, sg.q.e);
+    sg.q = QueryTiles(L, p.Q, iq, p.window, p.sinks);
+    sg.lo = max((int)(t - base) - start, 0);
+    const int end = (int)min(t_end - base, (long long)n);
+    sg.hi = min(max(end - start, 0), sg.q.e);
     t = base + end;
     return true;
   }
@@ -319,13 +261,13 @@ struct Ring {
 // visible row is not loaded (it need not be mapped).
 __device__ void producer_role(const AttendPackedParams &p, const Shared &sh, const CUtensorMap *tm_codes,
                               const CUtensorMap *tm_scales, int iq, int lane) {
-  const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.a.status};
+  const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.status};
   Ring raw;
   uint32_t issued = 0;
   SegIter it(*sh.range, iq);
   Segment sg;
   while (it.next(p, sg)) {
-    const int32_t *table = p.a.page_table + (long long)sg.b * p.a.max_pages;
+    const int32_t *table = p.page_table + (long long)sg.b * p.max_pages;
     const int count = sg.count();
     int n = sg.first();
     for (int k0 = 0; k0 < count; k0 += 16) {
@@ -337,8 +279,8 @@ __device__ void producer_role(const AttendPackedParams &p, const Shared &sh, con
         const int pg = sg.q.seq.tile(ahead) * (kTile / kPageTokens) + lane % 2;
         if (sg.q.any_row(pg * kPageTokens, kPageTokens)) {
           id = table[pg];
-          if (id < 0 || id >= p.a.num_pages) {
-            report_status(p.a.status, kStatusIndex);
+          if (id < 0 || id >= p.num_pages) {
+            report_status(p.status, kStatusIndex);
             id = 0;
           }
         }
@@ -366,12 +308,12 @@ __device__ void producer_role(const AttendPackedParams &p, const Shared &sh, con
     }
   }
 done:
-  if (lane == 0 && !drain_ring(&sh.bar[kBarRawFull], kRawSlots, issued)) report_status(p.a.status, kStatusTimeout);
+  if (lane == 0 && !drain_ring(&sh.bar[kBarRawFull], kRawSlots, issued)) report_status(p.status, kStatusTimeout);
 }
 
 // ------------------------------------------------------------------ MMA issuers (warps 1 and 2)
 __device__ void score_mma_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq) {
-  const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.a.status};
+  const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.status};
   constexpr uint32_t idesc = idesc_f16_f32(kTile, kHeads, false);
   const uint64_t b0 = sw128_desc(smem_u32(sh.base + kOffQ), 16, 1024);
   Ring st;
@@ -406,7 +348,7 @@ __device__ void score_mma_role(const AttendPackedParams &p, const Shared &sh, ui
 }
 
 __device__ void value_mma_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq) {
-  const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.a.status};
+  const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.status};
   constexpr uint32_t idesc = idesc_f16_f32(128, kHeads, true);
   const uint64_t b0 = sw128_desc(smem_u32(sh.base + kOffP), kPBytes, 1024);
   Ring st;
@@ -470,8 +412,9 @@ struct Stager {
 };
 
 // Thread = row.  A chunk is 64 latents: 32 bytes of codes, four scales, 32 columns.
-__device__ void unpack_rows_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, int wq, int lane) {
-  const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.a.status};
+__device__ void unpack_rows_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, int wq,
+                                 int lane) {
+  const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.status};
   const int row = wq * 32 + lane;
   const uint32_t raw0 = smem_u32(sh.base);
   const uint32_t code_off = row * 128 + ((row & 7) << 4);
@@ -528,8 +471,9 @@ __device__ __forceinline__ int k_of_row(int r) {  // K index of tile row r
   return (r & ~15) | ((r & 6) << 1) | ((r & 8) >> 2) | (r & 1);
 }
 
-__device__ void unpack_latents_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, int wq, int lane) {
-  const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.a.status};
+__device__ void unpack_latents_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int iq, int wq,
+                                    int lane) {
+  const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.status};
   const int g = lane >> 2, c = lane & 3;
   const int group = 8 * wq + g;
   // the group's eight bytes in a row: half, 16-byte unit, which eight of it; the thread's rows of
@@ -611,7 +555,7 @@ __device__ void unpack_latents_role(const AttendPackedParams &p, const Shared &s
 // an MMA result into a score in log2 units.  Warp w converts heads 8w .. 8w + 7, four at a time.
 __device__ __forceinline__ void convert_query(const AttendPackedParams &p, const Shared &sh, int b, int iq, int w,
                                               int lane) {
-  const uint16_t *q = p.q_tilde + ((long long)b * p.a.Q + iq) * kHeads * kLatent;
+  const uint16_t *q = p.q_tilde + ((long long)b * p.Q + iq) * kHeads * kLatent;
   const uint32_t dst = smem_u32(sh.base + kOffQ);
 #pragma unroll 1
   for (int h4 = 0; h4 < 8; h4 += 4) {
@@ -667,8 +611,9 @@ __device__ __forceinline__ float sum_columns(float (&v)[32], int lane) {
   return v[0];
 }
 
-__device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int grp, int iq, int warp, int lane) {
-  const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.a.status};
+__device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint32_t tmem, int grp, int iq, int warp,
+                             int lane) {
+  const Bars bar{smem_u32(sh.bar), sh.abort_flag, p.status};
   const int w = warp - 3, wg = w >> 2, wq = warp & 3;
   const int tid = wq * 32 + lane;    // within the warpgroup
   const int row = wq * 32 + lane;    // tile row = tensor-memory lane
@@ -683,12 +628,12 @@ __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint
   SegIter it(*sh.range, iq);
   Segment sg;
   while (it.next(p, sg)) {
-    const long long slot = split::partial_slot(p.a, kModePaged, grp, sg.b, iq);
+    const long long slot = split::partial_slot(p, kModePaged, grp, sg.b, iq);
     int n = sg.first();
     if (n >= sg.hi) {
       if (tid < 32) {
-        p.a.part_m[slot * kHeads + col0 + tid] = -INFINITY;
-        p.a.part_l[slot * kHeads + col0 + tid] = 0.f;
+        p.part_m[slot * kHeads + col0 + tid] = -INFINITY;
+        p.part_l[slot * kHeads + col0 + tid] = 0.f;
       }
       continue;
     }
@@ -717,9 +662,10 @@ __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float4 c4 = cs4[j], mm = m4[j];
-          fma_f32x2(x[4 * j], x[4 * j + 1], __uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1]), c4.x, c4.y, mm.x, mm.y);
-          fma_f32x2(x[4 * j + 2], x[4 * j + 3], __uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3]), c4.z, c4.w,
-                    mm.z, mm.w);
+          fma_f32x2(x[4 * j], x[4 * j + 1], __uint_as_float(s[4 * j]), __uint_as_float(s[4 * j + 1]), c4.x, c4.y, mm.x,
+                    mm.y);
+          fma_f32x2(x[4 * j + 2], x[4 * j + 3], __uint_as_float(s[4 * j + 2]), __uint_as_float(s[4 * j + 3]), c4.z,
+                    c4.w, mm.z, mm.w);
         }
       }
       if (!sg.q.every_row(j0, kTile)) {
@@ -743,7 +689,8 @@ __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint
         named_bar_sync(bar_id, 128);
         if (tid < 32) {
           const int h = col0 + tid;
-          const float mt = fmaxf(fmaxf(sh.red[h], sh.red[kHeads + h]), fmaxf(sh.red[2 * kHeads + h], sh.red[3 * kHeads + h]));
+          const float mt =
+              fmaxf(fmaxf(sh.red[h], sh.red[kHeads + h]), fmaxf(sh.red[2 * kHeads + h], sh.red[3 * kHeads + h]));
           float d = mt - kShift;  // how far m rises (the first tile sets it)
           if (mt == -INFINITY || (!first && d < 0.f)) d = 0.f;
           sh.rise[h] = d;
@@ -798,13 +745,13 @@ __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint
     named_bar_sync(bar_id, 128);
     if (tid < 32) {
       const int h = col0 + tid;
-      p.a.part_m[slot * kHeads + h] = -sh.m[h];
-      p.a.part_l[slot * kHeads + h] = sh.red[h] + sh.red[kHeads + h] + sh.red[2 * kHeads + h] + sh.red[3 * kHeads + h];
+      p.part_m[slot * kHeads + h] = -sh.m[h];
+      p.part_l[slot * kHeads + h] = sh.red[h] + sh.red[kHeads + h] + sh.red[2 * kHeads + h] + sh.red[3 * kHeads + h];
     }
     wait(bar, kBarOFull, segs & 1);
     __syncwarp();
     tc_fence_after();
-    float *po = p.a.part_o + slot * kHeads * kLatent;
+    float *po = p.part_o + slot * kHeads * kLatent;
 #pragma unroll 1
     for (int mb = 0; mb < 4; ++mb) {
       uint32_t o[32];
@@ -839,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   sh.abort_flag = reinterpret_cast<volatile int *>(sh.base + kOffMisc + 4);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int g = blockIdx.x / p.a.group_size, iq = blockIdx.x % p.a.group_size;
+  const int g = blockIdx.x / p.group_size, iq = blockIdx.x % p.group_size;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRawSlots; ++i) {
@@ -873,17 +820,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_dep_launch();
   grid_dep_wait();  // everything below may come from the previous kernel
-  if (blockIdx.x == 0 && warp == 2) warp_write_seq_prefix(p, lane);
   if (warp == 0) {
-    // this warp initialised the barriers and finds the range: it starts loading at once
-    const Range r = find_range(p, g, lane);
+    // This warp initialised the barriers and finds the range: it starts loading at once.  Not on
+    // barrier 0: with nothing to load it may be at the block's last barrier before the others
+    // are at this one.
+    const Range r = lists::find_range<Seqs>(p, g, lane);
     if (lane == 0) *range = r;
     __syncwarp();
-    asm volatile("bar.arrive 0, %0;" ::"n"(kThreads) : "memory");
+    asm volatile("bar.arrive 4, %0;" ::"n"(kThreads) : "memory");
     producer_role(p, sh, &tm_codes, &tm_scales, iq, lane);
   } else {
     tc_fence_before();
-    asm volatile("bar.sync 0, %0;" ::"n"(kThreads) : "memory");
+    asm volatile("bar.sync 4, %0;" ::"n"(kThreads) : "memory");
     tc_fence_after();
   }
   const uint32_t tmem = *sh.tmem_slot;
@@ -899,6 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 15) {
     unpack_rows_role(p, sh, tmem, iq, warp & 3, lane);
   } else {
+    if (blockIdx.x == 0 && warp == 15) lists::write_partial_table<Seqs>(p, lane);  // C^T is needed last: there is time
     unpack_latents_role(p, sh, tmem, iq, warp & 3, lane);
   }
 
@@ -914,91 +863,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (*sh.abort_flag) {
       if (lane == 0) {
         umma_commit(&sh.bar[kBarDrain]);
-        if (!mbar_wait_drain(&sh.bar[kBarDrain], 0)) report_status(p.a.status, kStatusTimeout);
+        if (!mbar_wait_drain(&sh.bar[kBarDrain], 0)) report_status(p.status, kStatusTimeout);
       }
       __syncwarp();
     }
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
-  }
-}
-
-// ------------------------------------------------------------------ combine
-// One block per (query row, two heads); thread t merges latents 4t .. 4t + 3 of both from the
-// row's partials: with M the largest running max, O = sum 2^(m_k - M) O_k and l likewise, then
-// unit * O / l and lse = (M + log2 l) ln 2.  A partial is in (block, lane) order: the four
-// values of a thread are four words apart by eight, and a warp's loads cover whole sectors.
-constexpr int kCombineHeads = 2, kCombineChunk = 3;
-
-__global__ void __launch_bounds__(128, 8) combine_packed_kernel(const AttendPackedParams p) {
-  grid_dep_launch();
-  grid_dep_wait();
-  const int v = blockIdx.x, b = v / p.a.Q, i = v % p.a.Q, tid = threadIdx.x;
-  __shared__ split::GroupRange sh_gr;
-  if (tid == 0) {
-    sh_gr = split::seq_group_range(p.a, kModePaged, b);
-    if (blockIdx.y == 0 && i == 0) {
-      const int L = p.a.seq_lens[b];
-      if (L < 0 || L > p.a.max_pages * kPageTokens) report_status(p.a.status, kStatusIndex);
-    }
-  }
-  __syncthreads();
-  const split::GroupRange gr = sh_gr;
-  const int h0 = blockIdx.y * kCombineHeads;
-  const int idx = partial_index(4 * tid);
-  float M[kCombineHeads], den[kCombineHeads], acc[kCombineHeads][4];
-#pragma unroll
-  for (int hh = 0; hh < kCombineHeads; ++hh) {
-    M[hh] = -INFINITY;
-    den[hh] = acc[hh][0] = acc[hh][1] = acc[hh][2] = acc[hh][3] = 0.f;
-  }
-  for (int k0 = 0; k0 < gr.count; k0 += kCombineChunk) {
-    float mk[kCombineHeads][kCombineChunk], lk[kCombineHeads][kCombineChunk], ok[kCombineHeads][kCombineChunk][4];
-#pragma unroll
-    for (int j = 0; j < kCombineChunk; ++j) {
-      const int k = k0 + j;
-      const bool live = k < gr.count;
-      const long long slot = live ? split::partial_slot(p.a, kModePaged, gr.partial_group(k), b, i) : 0;
-#pragma unroll
-      for (int hh = 0; hh < kCombineHeads; ++hh) {
-        const long long r = slot * kHeads + h0 + hh;
-        mk[hh][j] = live ? p.a.part_m[r] : -INFINITY;
-        lk[hh][j] = live ? p.a.part_l[r] : 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ok[hh][j][e] = live ? p.a.part_o[r * kLatent + idx + 8 * e] : 0.f;
-      }
-    }
-#pragma unroll
-    for (int hh = 0; hh < kCombineHeads; ++hh) {
-      float mx = M[hh];
-#pragma unroll
-      for (int j = 0; j < kCombineChunk; ++j) mx = fmaxf(mx, mk[hh][j]);
-      if (mx == -INFINITY) continue;
-      const float a = exp2f(M[hh] - mx);  // 0 when M was -inf
-      den[hh] *= a;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[hh][e] *= a;
-#pragma unroll
-      for (int j = 0; j < kCombineChunk; ++j) {
-        if (mk[hh][j] == -INFINITY) continue;  // an empty partial's O was never written
-        const float wt = exp2f(mk[hh][j] - mx);
-        den[hh] += wt * lk[hh][j];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[hh][e] += wt * ok[hh][j][e];
-      }
-      M[hh] = mx;
-    }
-  }
-#pragma unroll
-  for (int hh = 0; hh < kCombineHeads; ++hh) {
-    const bool seen = M[hh] != -INFINITY;
-    const float inv = seen ? p.unit / den[hh] : 0.f;
-    uint2 out;
-    out.x = pack_bf16x2(acc[hh][0] * inv, acc[hh][1] * inv);
-    out.y = pack_bf16x2(acc[hh][2] * inv, acc[hh][3] * inv);
-    *reinterpret_cast<uint2 *>(p.a.o_latent + ((long long)v * kHeads + h0 + hh) * kLatent + 4 * tid) = out;
-    if (p.a.lse != nullptr && tid == 0)
-      p.a.lse[(long long)v * kHeads + h0 + hh] = seen ? (M[hh] + log2f(den[hh])) * 0.69314718055994530942f : -INFINITY;
   }
 }
 
@@ -1010,12 +880,11 @@ cudaError_t launch_attend_packed(const CUtensorMap &tm_codes, const CUtensorMap 
   if (cudaError_t e = set_smem_limit_once(packed::attend_packed_kernel, packed::kSmemBytes, configured_device);
       e != cudaSuccess)
     return e;
-  if (cudaError_t e = launch_chained(packed::attend_packed_kernel, dim3(p.a.groups * p.a.group_size),
+  if (cudaError_t e = launch_chained(packed::attend_packed_kernel, dim3(p.groups * p.group_size),
                                      dim3(packed::kThreads), packed::kSmemBytes, stream, tm_codes, tm_scales, p);
       e != cudaSuccess)
     return e;
-  return launch_chained(packed::combine_packed_kernel, dim3(p.a.B * p.a.Q, kHeads / packed::kCombineHeads), dim3(128), 0,
-                        stream, p);
+  return lists::launch_combine<packed::Seqs, packed::PartialOrder>(p, p.unit, stream);
 }
 
 }  // namespace mla

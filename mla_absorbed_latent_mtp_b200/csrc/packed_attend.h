@@ -5,8 +5,7 @@
 
 namespace mla {
 
-struct AttendPackedParams {
-  AttendParams a;             // sizes, seq_lens, page_table, workspace parts, outputs, status
+struct AttendPackedParams : AttendParams {
   const uint16_t *q_tilde;    // [B, Q, H, R]
   int window, sinks;          // window 0: every row up to the query's own
   float unit;                 // c = unit * scale * code

@@ -4,15 +4,15 @@
 //
 // The pipeline is attend.cu's (64-row tiles, a ring of 2.25 tiles in shared memory filled by TMA,
 // scores and value products on tcgen05 from two issuing warps, eight softmax warps, lazy rescale
-// of O in tensor memory, partials merged by its combine kernel).  It is a kernel of its own
+// of O in tensor memory).  It is a kernel of its own
 // because the window's bookkeeping, as a template parameter of that kernel, changed the code
 // generated for the other modes and cost a verify step 1.5%.  What differs:
 //  - a sequence's tile list holds only the tiles of its sinks and of its queries' windows, so the
 //    work is split evenly over what has to be read; a query walks those of them that it sees;
 //  - rows that a query does not see are masked in the softmax, and zeroed in the landed slot,
 //    whatever they hold;
-//  - one warp finds a CTA's first sequence by a scan (a walk costs the last CTAs of a 32-sequence
-//    step two microseconds);
+//  - the list's ranges allow for what beginning a sequence costs, and the merge has a form for few
+//    sequences with many partials (lists.cuh);
 //  - l sums the unrounded weights, so lse is exact to fp32.
 //
 // What bounds it: as attend.cu, the recycling of ring slots, 3,000 cycles a tile (0.87 of the
@@ -23,6 +23,7 @@
 #include <algorithm>
 
 #include "internal.h"
+#include "lists.cuh"
 #include "window_attend.h"
 #include "sm100.cuh"
 #include "split.cuh"
@@ -59,7 +60,7 @@ constexpr int kBarCFull = 0, kBarCEmpty = kSlots, kBarQFull = 2 * kSlots, kBarQE
               kBarDrain = kBarOEmpty + 1, kNumBars = kBarDrain + 1;
 constexpr int kOffMisc = kOffBar + kNumBars * 8;
 constexpr int kOffRange = kOffMisc + 16;
-constexpr int kSmemUsed = kOffRange + 32;
+constexpr int kSmemUsed = kOffRange + (int)sizeof(lists::Range);
 constexpr int kSmemBytes = kSmemUsed + 1024;  // slack for 1024-byte alignment of the base
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(kPageTokens == kTile, "a paged tile is exactly one page");
@@ -72,83 +73,25 @@ constexpr uint32_t kTmemO = 256;
 
 // ------------------------------------------------------------------ sequences and tiles
 
-// Rows of sequence b.
-template <bool kPaged>
-__device__ __forceinline__ int seq_rows(const WindowParams &p, int b) {
-  const int L = p.seq_lens ? p.seq_lens[b] : p.Lmax;
-  return min(max(L, 0), kPaged ? p.max_pages * kPageTokens : p.Lmax);
-}
-using split::group_start;
 using SeqTiles = window::SeqTiles<kTile>;
 using QueryTiles = window::QueryTiles<kTile>;
 template <bool kPaged>
-__device__ __forceinline__ int seq_tiles(const WindowParams &p, int b) {
-  return SeqTiles(seq_rows<kPaged>(p, b), p.Q, p.window, p.sinks).count;
-}
-
-// Total tiles over all sequences (computed by one warp).
-template <bool kPaged>
-__device__ long long warp_total_tiles(const WindowParams &p, int lane) {
-  long long acc = 0;
-  for (int b = lane; b < p.B; b += 32) acc += seq_tiles<kPaged>(p, b);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-  return acc;
-}
-
-// Position of every sequence in the tile list (first tile, tile count), for the combine
-// (computed by one warp with an exclusive scan in steps of 32 sequences).
-template <bool kPaged>
-__device__ void warp_write_seq_prefix(const WindowParams &p, int lane) {
-    long long base = 0;
-  for (int s0 = 0; s0 < p.B; s0 += 32) {
-    const int s = s0 + lane;
-    const int nt = s < p.B ? seq_tiles<kPaged>(p, s) : 0;
-    long long x = nt;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (s < p.B) {
-      p.seq_ts[s] = base + x - nt;
-      p.seq_nt[s] = nt;
-    }
-    base += __shfl_sync(0xffffffffu, x, 31);
+struct Seqs {  // for lists.cuh
+  static constexpr int kStart = 3;
+  static __device__ __forceinline__ int cap(const WindowParams &p) {
+    return kPaged ? p.max_pages * kPageTokens : p.Lmax;
   }
-}
-
-// A CTA's range [t0, t1) of the tile list, the sequence s that holds its first tile and the first tile
-// of that sequence; by one warp's scans in steps of 32 sequences.
-struct Range {
-  long long t0, t1, base;
-  int s;
+  static __device__ __forceinline__ int length(const WindowParams &p, int b) {
+    return min(max(p.seq_lens ? p.seq_lens[b] : p.Lmax, 0), cap(p));
+  }
+  static __device__ __forceinline__ int tiles(const WindowParams &p, int L) {
+    return SeqTiles(L, p.Q, p.window, p.sinks).count;
+  }
+  static __device__ __forceinline__ bool bad_length(const WindowParams &p, int b) {
+    return p.seq_lens && (p.seq_lens[b] < 0 || p.seq_lens[b] > cap(p));
+  }
 };
-static_assert(sizeof(Range) <= 32, "kOffRange");
-template <bool kPaged>
-__device__ Range warp_find(const WindowParams &p, int g, int lane) {
-  const long long T = warp_total_tiles<kPaged>(p, lane);
-  Range r = {group_start(g, T, p.groups), group_start(g + 1, T, p.groups), 0, 0};
-  if (r.t0 >= r.t1) return r;
-  for (int s0 = 0; s0 < p.B; s0 += 32) {
-    const int nt = s0 + lane < p.B ? seq_tiles<kPaged>(p, s0 + lane) : 0;
-    int x = nt;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    const uint32_t ends_behind = __ballot_sync(0xffffffffu, r.base + x > r.t0);
-    if (ends_behind) {
-      const int l = __ffs(ends_behind) - 1;
-      r.s = s0 + l;
-      r.base += __shfl_sync(0xffffffffu, x - nt, l);
-      break;
-    }
-    r.base += __shfl_sync(0xffffffffu, x, 31);
-  }
-  return r;
-}
+using lists::Range;
 
 // A segment: the piece of sequence s in a CTA's range.  lo, hi and the loops' t count list tiles, of
 // which next() skips those that the query does not see; tile(t) is the tile of the sequence.
@@ -165,25 +108,30 @@ struct Seg {
 template <bool kPaged>
 struct SegIter {
   long long t, t_end, base;
-  int s, iq;
-  __device__ SegIter(const Range &r, int iq_) : t(r.t0), t_end(r.t1), base(r.base), s(r.s), iq(iq_) {}
+  int s, L, start, iq;
+  __device__ SegIter(const Range &r, int iq_)
+      : t(r.t0), t_end(r.t1), base(r.base), s(r.s), L(r.L), start(r.start), iq(iq_) {}
   __device__ bool next(const WindowParams &p, Seg &sg) {
     if (t >= t_end) return false;
-    int nt = seq_tiles<kPaged>(p, s);
-    while (base + nt <= t) {
-      base += nt;
-      ++s;
-      nt = seq_tiles<kPaged>(p, s);
+    int n = lists::places<Seqs<kPaged>>(p, L, start);
+    while (base + n <= t) {
+      base += n;
+      L = Seqs<kPaged>::length(p, ++s);
+      n = lists::places<Seqs<kPaged>>(p, L, start);
     }
-    const long long end = min(t_end - base, (long long)nt);
+    const int end = (int)min(t_end - base, (long long)n);
     sg.s = s;
-    sg.q = QueryTiles(seq_rows<kPaged>(p, s), p.Q, iq, p.window, p.sinks);
-    sg.lo = sg.q.seek((int)(t - base));
-    sg.hi = min((int)end, sg.q.e);
+    sg.q = QueryTiles(L, p.Q, iq, p.window, p.sinks);
+    sg.lo = sg.q.seek(max((int)(t - base) - start, 0));
+    sg.hi = min(max(end - start, 0), sg.q.e);
     sg.empty = sg.hi <= sg.lo;
     t = base + end;
     return true;
   }
+};
+
+struct PartialOrder {  // partials are stored latent by latent
+  static __device__ __forceinline__ int latent(int idx) { return idx; }
 };
 
 // ------------------------------------------------------------------ shared state
@@ -619,22 +567,23 @@ __global__ void __launch_bounds__(384, 1)
   }
   grid_dep_launch();
   grid_dep_wait();  // inputs (q~, lengths, tables, cache) may come from the previous kernel
-  if (blockIdx.x == 0 && warp == 2) warp_write_seq_prefix<kPaged>(p, lane);
   Range *range = reinterpret_cast<Range *>(base + kOffRange);
   if (warp == 0) {
-    // this warp initialised the barriers and finds the CTA's range: it starts loading at once
-    const Range r = warp_find<kPaged>(p, g, lane);
+    // This warp initialised the barriers and finds the CTA's range: it starts loading at once.  Not on
+    // barrier 0: with nothing to load it may be at the block's last barrier before the others
+    // are at this one.
+    const Range r = lists::find_range<Seqs<kPaged>>(p, g, lane);
     if (lane == 0) {
       *range = r;
       prefetch_tensormap(&tm_qt);
       prefetch_tensormap(&tm_cache);
     }
     __syncwarp();
-    asm volatile("bar.arrive 0, %0;" ::"n"(kThreads) : "memory");
+    asm volatile("bar.arrive 4, %0;" ::"n"(kThreads) : "memory");
     if (lane == 0) producer_role<kPaged>(p, sh, &tm_cache, &tm_qt, iq, r);
   } else {
     tc_fence_before();
-    asm volatile("bar.sync 0, %0;" ::"n"(kThreads) : "memory");
+    asm volatile("bar.sync 4, %0;" ::"n"(kThreads) : "memory");
     tc_fence_after();
   }
   const uint32_t tmem = *sh.tmem_slot;
@@ -645,6 +594,7 @@ __global__ void __launch_bounds__(384, 1)
   } else if (warp == 1) {
     score_mma_role<kPaged>(p, sh, tmem, iq, r, lane);
   } else if (warp == 10) {
+    if (blockIdx.x == 0) lists::write_partial_table<Seqs<kPaged>>(p, lane);  // needed last: there is time
     value_mma_role<kPaged>(p, sh, tmem, iq, r);
   } else {
     softmax_role<kPaged>(p, sh, tmem, g, iq, r, warp, lane);
@@ -675,11 +625,6 @@ __global__ void __launch_bounds__(384, 1)
 
 }  // namespace windowed
 
-// attend.cu's combine
-namespace attend {
-__global__ void combine_kernel(const AttendParams p, int mode);
-}
-
 template <bool kPaged>
 static cudaError_t launch_window(const CUtensorMap &tm_cache, const CUtensorMap &tm_qt, const WindowParams &p,
                                  cudaStream_t stream) {
@@ -691,9 +636,7 @@ static cudaError_t launch_window(const CUtensorMap &tm_cache, const CUtensorMap 
                                      dim3(windowed::kThreads), windowed::kSmemBytes, stream, tm_cache, tm_qt, p);
       e != cudaSuccess)
     return e;
-  const AttendParams &a = p;
-  return launch_chained(attend::combine_kernel, dim3(p.B * p.Q, kHeads / 2), dim3(128), 0, stream, a,
-                        (int)(kPaged ? kModePaged : kModeDense));
+  return lists::launch_combine<windowed::Seqs<kPaged>, windowed::PartialOrder>(p, 1.f, stream);
 }
 
 cudaError_t launch_attend_window(bool paged, const CUtensorMap &tm_cache, const CUtensorMap &tm_qt,
