@@ -11,7 +11,10 @@
 // measured back to back), with its A operand in tensor memory 32.4, the full rate; and 4-bit
 // codes cannot be an operand as they are, since each row has its own scales.  So the cache
 // operand is unpacked into TENSOR memory, twice, by register, and shared memory holds only the
-// packed rows, q~ and P:
+// packed rows, q~ and P.  Measured: 5,300 cycles a tile, 2.6 times the MMAs' own; the rest is the
+// unpacking, the softmax and the hand-overs between them (3,070 instructions a tile and scheduler).
+// With the merge 32 x 8,192 rows take 67 us, 16 sequences of 1.05 M rows in all 192 us, 16 x 6
+// queries with a window of 8,191 rows and 64 sinks 144 us.
 //   S^T[rows, heads]    = C (A: 128 rows on the lanes, 64 latents a chunk) * Q~^T (smem)
 //   O^T[latent, heads] += C^T (A: 128 latents on the lanes, 16 rows a chunk, x 4) * P^T (smem)
 // Both unpackings read the same packed words.  For C a thread owns a row.  For C^T a thread
@@ -388,9 +391,10 @@ __device__ void value_mma_role(const AttendPackedParams &p, const Shared &sh, ui
 
 // ------------------------------------------------------------------ unpack C (warps 11-14)
 // Both unpackers read the next chunk's words from shared memory before they convert this one's
-// (the last chunk reads the first again, to no use).  The chunk loops stay rolled: with five kinds
-// of warps on a scheduler, unrolled bodies missed the instruction cache (32 x 8,192 rows: 117 us
-// with the chunks unrolled).
+// (the last chunk reads the first again, to no use).  The chunk loops are unrolled by two: with
+// five kinds of warps on a scheduler, fully unrolled bodies missed the instruction cache (32 x
+// 8,192 rows: 117 us with all eight chunks unrolled, 78 rolled when that was tried; 16 ragged
+// sequences later 218 us rolled, 211 by two).
 struct Stager {
   Bars bar;
   uint32_t full, empty;  // barrier indexes of slot 0

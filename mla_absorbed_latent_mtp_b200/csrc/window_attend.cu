@@ -4,9 +4,9 @@
 //
 // The pipeline is attend.cu's (64-row tiles, a ring of 2.25 tiles in shared memory filled by TMA,
 // scores and value products on tcgen05 from two issuing warps, eight softmax warps, lazy rescale
-// of O in tensor memory).  It is a kernel of its own
-// because the window's bookkeeping, as a template parameter of that kernel, changed the code
-// generated for the other modes and cost a verify step 1.5%.  What differs:
+// of O in tensor memory).  It is a kernel of its own because the window's bookkeeping, as a
+// template parameter of that kernel, changed the code generated for the other modes and cost a
+// verify step 1.5%.  What differs:
 //  - a sequence's tile list holds only the tiles of its sinks and of its queries' windows, so the
 //    work is split evenly over what has to be read; a query walks those of them that it sees;
 //  - rows that a query does not see are masked in the softmax, and zeroed in the landed slot,
@@ -17,7 +17,8 @@
 //
 // What bounds it: as attend.cu, the recycling of ring slots, 3,000 cycles a tile (0.87 of the
 // measured copy peak for distinct rows); around that, for windows of some thousand rows, 20 us of
-// start-up, partial stores and combine.
+// start-up, partial stores and combine.  Measured with the merge: 32 x (4,096 + 64) of 8,192 rows
+// 41.7 us; 16 x 6 queries, window 4,095 + 5, 89-91 us.
 #include <math.h>
 
 #include <algorithm>
