@@ -223,23 +223,25 @@ __device__ void copy_page(const Book &bk, int dst, int src) {
   }
 }
 
-// Pages taken by list entries before k (refused ones take none), by the whole block.
-__device__ int demand_before(const Book &bk, int k) {
-  __shared__ int total;
+// Pages taken by list entries before k (refused ones take none), by the whole block.  In 64 bits:
+// a list of 66 sequences can ask for 2^31 pages.
+__device__ long long demand_before(const Book &bk, int k) {
+  __shared__ unsigned long long total;
   if (threadIdx.x == 0) total = 0;
   __syncthreads();
-  int n = 0;
+  unsigned long long n = 0;
   for (int i = threadIdx.x; i < k; i += kThreads) n += max(bk.demand[i], 0);
-  n = __reduce_add_sync(0xffffffffu, n);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   if (threadIdx.x % 32 == 0 && n) atomicAdd(&total, n);
   __syncthreads();
-  return total;
+  return (long long)total;
 }
 
 // True if entry k goes ahead; reports why it does not.
-__device__ bool granted(const Book &bk, const int32_t *rank, int k, int before) {
+__device__ bool granted(const Book &bk, const int32_t *rank, int k, long long before) {
   const int d = bk.demand[k];
-  const bool room = d <= 0 || (long long)before + d <= rank[bk.nchunks];
+  const bool room = d <= 0 || before + d <= rank[bk.nchunks];
   if (threadIdx.x == 0) {
     if (d == kBad) report_status(bk.status, kStatusIndex);
     else if (!room) report_status(bk.status, kStatusPages);
@@ -255,8 +257,9 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const Book bk, int Q)
   const int b = blockIdx.x;
   if (bk.demand[b] == 0) return;
   load_ranks(bk, rank);
-  int next = demand_before(bk, b);
-  if (!granted(bk, rank, b, next)) return;
+  const long long taken = demand_before(bk, b);
+  if (!granted(bk, rank, b, taken)) return;
+  int next = (int)taken;  // below the number of free pages
   int first, end;
   reserve_range(bk, b, Q, first, end);
   int32_t *row = bk.table + (long long)b * bk.max_pages;
@@ -296,13 +299,14 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const Book bk, int Q)
 }
 
 // Block k: fork k.
-__global__ void __launch_bounds__(kThreads) fork_kernel(const Book bk, const int32_t *parents, const int32_t *children) {
+__global__ void __launch_bounds__(kThreads) fork_kernel(const Book bk, const int32_t *parents,
+                                                        const int32_t *children) {
   extern __shared__ int32_t rank[];
   grid_dep_launch();
   grid_dep_wait();
   const int k = blockIdx.x;
   load_ranks(bk, rank);
-  const int before = demand_before(bk, k);
+  const long long before = demand_before(bk, k);
   if (!granted(bk, rank, k, before)) return;
   const int par = parents[k], child = children[k];
   const int L = bk.lens[par];
@@ -318,7 +322,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const Book bk, const int
   if (threadIdx.x == 0) {
     bk.lens[child] = L;
     if (L % kPageTokens) {
-      fresh = nth_page<false>(bk, rank, before);
+      fresh = nth_page<false>(bk, rank, (int)before);
       to[full] = fresh;
       bk.refs[fresh] = 1;
     }

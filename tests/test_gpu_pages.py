@@ -212,3 +212,19 @@ def test_bf16_pool_and_attention_after_a_fork_and_a_compaction():
     assert (after[2].float() - before[0].float()).abs().max() <= 2.0 ** -7 * before[0].float().abs().max()
     # the child's copy is its own
     assert int(s.table[2, 3].item()) != int(s.table[0, 3].item()) and torch.equal(s.table[2, :3], s.table[0, :3])
+
+
+def test_demands_past_32_bits():
+    """66 sequences that ask for 2^25 - 1 pages each: their sum passes 2^31, none has room, and
+    nothing changes."""
+    B, max_pages, P = 66, 2 ** 25 - 1, 64
+    table = torch.full((B, max_pages), -1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    refs = torch.zeros(P, dtype=torch.int32, device="cuda")
+    pool = torch.zeros(P, PAGE, 16, dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    m.mla_pages_reserve(pool, table, lens, refs, max_pages * PAGE, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == m.MLA_ERR_PAGES
+    assert int(refs.abs().max().item()) == 0
+    assert int(table.amax().item()) == -1 and int(table.amin().item()) == -1
