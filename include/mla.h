@@ -330,7 +330,8 @@ mla_status mla_attend_packed(const uint16_t *q_tilde, const uint8_t *pool, const
  *   seq_lens[b] = 0, all of a sequence.
  * mla_pages_compact: moves the pages that are used (refs > 0) and lie at or above n_used, their
  *   number, to the free pages below it, in order; refs and all B tables follow.  n_used: device int32.
- *   Afterwards pages n_used .. num_pages - 1 are free.
+ *   Afterwards pages n_used .. num_pages - 1 are free.  An entry that maps a free page stays as it is
+ *   and sets MLA_ERR_INDEX.
  * A sequence or list entry whose positions, pages or indexes are out of range (or, fork: as above) is
  * left untouched and sets MLA_ERR_INDEX; one whose pages are no longer free, and every later one
  * that needs a page, is left untouched and sets MLA_ERR_PAGES; the others proceed.  Pages keep

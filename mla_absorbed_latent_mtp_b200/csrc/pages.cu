@@ -369,13 +369,13 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const Book bk, int32_
   const int kept = n_used - moves;  // used pages below n_used
   if (blockIdx.x == 0 && threadIdx.x == 0) *n_used_out = n_used;
   const long long entries = (long long)bk.B * bk.max_pages;
-  for (long long e = (long long)blockIdx.x * kThreads + threadIdx.x; e < entries; e += (long long)gridDim.x * kThreads) {
+  const long long step = (long long)gridDim.x * kThreads;
+  for (long long e = (long long)blockIdx.x * kThreads + threadIdx.x; e < entries; e += step) {
     const int page = bk.table[e];
-    if (page < -1 || page >= bk.num_pages) report_status(bk.status, kStatusIndex);
-    else if (page >= n_used) {
-      if (bk.free_bits[page / 32] >> (page % 32) & 1) report_status(bk.status, kStatusIndex);  // mapped, but free
-      else bk.table[e] = nth_page<false>(bk, rank, page - free_below(bk, rank, page) - kept);
-    }
+    if (page == -1) continue;
+    // outside the pool, or mapped but free: the entry stays, whatever moves to that page
+    if (!mapped(bk, page) || (bk.free_bits[page / 32] >> (page % 32) & 1)) report_status(bk.status, kStatusIndex);
+    else if (page >= n_used) bk.table[e] = nth_page<false>(bk, rank, page - free_below(bk, rank, page) - kept);
   }
   for (int m = blockIdx.x; m < moves; m += gridDim.x) {
     const int src = nth_page<true>(bk, rank, kept + m), dst = nth_page<false>(bk, rank, m);
@@ -464,7 +464,8 @@ mla_status mla_pages_fork(void *pool, int page_bytes, int32_t *page_table, int32
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = launch_chained(snapshot_kernel<kFork>, dim3(bk.nchunks + n), dim3(kThreads), 0, st, bk, parents,
                                  children, n, 0);
-  if (e == cudaSuccess) e = launch_chained(fork_kernel, dim3(n), dim3(kThreads), rank_bytes(bk), st, bk, parents, children);
+  if (e == cudaSuccess)
+    e = launch_chained(fork_kernel, dim3(n), dim3(kThreads), rank_bytes(bk), st, bk, parents, children);
   return record_cuda_error(e);
 }
 
@@ -474,8 +475,8 @@ mla_status mla_pages_release(int32_t *page_table, const int32_t *seq_lens, int32
   using namespace mla::pages;
   if (seq_lens == nullptr) return MLA_ERR_ARG;
   Book bk;
-  if (mla_status s = make_book(bk, nullptr, 0, page_table, const_cast<int32_t *>(seq_lens), refs, B, max_pages, num_pages,
-                               B, nullptr, 0, status);
+  if (mla_status s = make_book(bk, nullptr, 0, page_table, const_cast<int32_t *>(seq_lens), refs, B, max_pages,
+                               num_pages, B, nullptr, 0, status);
       s != MLA_OK)
     return s;
   const int splits = std::min(64, (max_pages + kThreads - 1) / kThreads);

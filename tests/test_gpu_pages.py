@@ -228,3 +228,20 @@ def test_demands_past_32_bits():
     assert int(status.item()) == m.MLA_ERR_PAGES
     assert int(refs.abs().max().item()) == 0
     assert int(table.amax().item()) == -1 and int(table.amin().item()) == -1
+
+
+@pytest.mark.parametrize("low", [True, False])
+def test_compaction_flags_entries_that_map_free_pages(low):
+    """Below and above the pages in use: the entry stays, the status says so."""
+    refs = torch.ones(10, dtype=torch.int32, device="cuda")
+    page = 1 if low else 9
+    refs[page] = refs[2] = 0
+    table = torch.tensor([[0, 3, 4, 5], [6, 7, 8, page], [9 if low else 1, -1, -1, -1]], dtype=torch.int32, device="cuda")
+    pool = torch.arange(10, dtype=torch.uint8, device="cuda")[:, None, None].repeat(1, PAGE, 16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    n = m.mla_pages_compact(pool, table, refs, status=status)
+    torch.cuda.synchronize()
+    assert int(n.item()) == 8 and int(status.item()) == m.MLA_ERR_INDEX and int(table[1, 3].item()) == page
+    # used pages at or above 8 move, in order, to the free ones: low {8, 9} to {1, 2}, else {8} to {2}
+    assert table[1, 2].item() == (1 if low else 2) and table[2, 0].item() == (2 if low else 1)
+    assert int(pool[int(table[1, 2].item()), 0, 0].item()) == 8
