@@ -94,7 +94,8 @@ def lib():
     L.mla_attend_window_dense.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, f32, i32, i32, vp, sz, vp, vp, vp, vp]
     L.mla_attend_window_paged.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, f32, i32, i32, vp, sz, vp,
                                           vp, vp, vp]
-    for name in ("mla_attend_window_dense", "mla_attend_window_paged", "mla_cache_append_packed", "mla_cache_truncate_packed", "mla_cache_unpack", "mla_attend_packed",
+    for name in ("mla_attend_window_dense", "mla_attend_window_paged", "mla_cache_append_packed",
+                 "mla_cache_truncate_packed", "mla_cache_unpack", "mla_attend_packed",
                  "mla_pages_reserve", "mla_pages_fork", "mla_pages_release", "mla_pages_compact"):
         getattr(L, name).restype = ctypes.c_int32
     for name in ("mla_absorb_q", "mla_up_proj", "mla_attend_dense", "mla_attend_paged", "mla_attend_indexed",
@@ -162,6 +163,13 @@ def _check_current(*tensors):
     dev = _check_cuda(*tensors)
     if dev != _get_torch().cuda.current_device():
         raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{_torch.cuda.current_device()}")
+
+
+def _require_int32(**values):
+    """ctypes would wrap a larger number without a word."""
+    for name, v in values.items():
+        if isinstance(v, int) and not -2**31 <= v < 2**31:
+            raise ValueError(f"{name} must fit 32 bits, got {v}")
 
 
 def _used_on(stream, *tensors):
@@ -342,6 +350,7 @@ def mla_attend_indexed(q_tilde, cache, indices, seq_lens=None, scale=SCALE, work
 def mla_attend_window_dense(q_tilde, cache, window, sinks=0, seq_lens=None, scale=SCALE, workspace=None, o_latent=None,
                             lse=None, status=None, want_lse=True, stream=None):
     """mla_attend_dense where each query sees its last `window` rows and the first `sinks` ones."""
+    _require_int32(window=window, sinks=sinks)
     B, Q = _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens)
     _require(cache, "cache", "bf16", (None, None, R))
     if cache.shape[0] < B:
@@ -359,6 +368,7 @@ def mla_attend_window_dense(q_tilde, cache, window, sinks=0, seq_lens=None, scal
 def mla_attend_window_paged(q_tilde, pool, page_table, seq_lens, window, sinks=0, scale=SCALE, workspace=None,
                             o_latent=None, lse=None, status=None, want_lse=True, stream=None):
     """Paged counterpart of mla_attend_window_dense (pool [P, 64, R], page_table [B, max_pages])."""
+    _require_int32(window=window, sinks=sinks)
     B, Q = _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens, seq_lens_required=True)
     _require(pool, "pool", "bf16", (None, PAGE, R))
     _require(page_table, "page_table", "i32", (None, None))
@@ -584,6 +594,7 @@ def mla_cache_append_packed(pool, page_table, seq_lens, rows, unit=1.0, status=N
 
 def mla_cache_truncate_packed(pool, page_table, seq_lens, keep, q_len, status=None, stream=None):
     """Keep the first keep[b] of the last q_len rows of each sequence of a 4-bit pool; zero the rest."""
+    _require_int32(q_len=q_len)
     _require(seq_lens, "seq_lens", "i32", (None,))
     B = seq_lens.shape[0]
     _require(keep, "keep", "i32", min_numel=B)
@@ -596,6 +607,7 @@ def mla_cache_truncate_packed(pool, page_table, seq_lens, keep, q_len, status=No
 
 def mla_cache_unpack(pool, page_table, start, n, unit=1.0, rows=None, status=None, stream=None):
     """The values of positions start[b] .. start[b] + n - 1 of a 4-bit pool: rows [B, n, R] bf16."""
+    _require_int32(n=n)
     torch = _get_torch()
     _require(start, "start", "i32", (None,))
     B = start.shape[0]
@@ -615,6 +627,7 @@ def mla_attend_packed(q_tilde, pool, page_table, seq_lens, unit=1.0, window=0, s
                       o_latent=None, lse=None, status=None, want_lse=True, stream=None):
     """Attention over a 4-bit pool [P, 64, 288] uint8; with window > 0 each query sees its last
     `window` rows and the first `sinks` ones."""
+    _require_int32(window=window, sinks=sinks)
     B, Q = _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens, seq_lens_required=True)
     _check_packed(pool, page_table, B, "q_tilde", status)
     _check_current(q_tilde, pool, page_table, seq_lens, workspace, o_latent, lse, status)
@@ -629,6 +642,7 @@ def mla_attend_packed(q_tilde, pool, page_table, seq_lens, unit=1.0, window=0, s
 
 
 def mla_pages_workspace_bytes(n: int, num_pages: int) -> int:
+    _require_int32(n=n, num_pages=num_pages)
     return int(lib().mla_pages_workspace_bytes(n, num_pages))
 
 
@@ -646,7 +660,7 @@ def _check_pages(page_table, refs, status, seq_lens=None, lens_required=True):
 
 
 def _check_page_pool(pool, refs, n, workspace):
-    """pool [P, 64, ...] of any dtype, contiguous; returns (bytes per page, workspace)."""
+    """pool [P, 64, ...] of any dtype, contiguous; returns the bytes per page."""
     if pool is None or not pool.is_contiguous() or pool.dim() < 2 or pool.shape[1] != PAGE:
         raise ValueError(f"pool must be a contiguous [P, {PAGE}, ...] tensor")
     P = int(pool.shape[0])
@@ -654,11 +668,14 @@ def _check_page_pool(pool, refs, n, workspace):
         raise ValueError(f"refs must have one element per page ({P}), got {refs.numel()}")
     if workspace is not None:
         _require(workspace, "workspace", "u8", min_numel=mla_pages_workspace_bytes(n, P))
-    return pool.numel() * pool.element_size() // max(P, 1)
+    page_bytes = pool.numel() * pool.element_size() // max(P, 1)
+    _require_int32(page_bytes=page_bytes)
+    return page_bytes
 
 
 def mla_pages_reserve(pool, page_table, seq_lens, refs, q_len, workspace=None, status=None, stream=None):
     """Map pages for the next q_len rows of every sequence; shared pages among them become own copies."""
+    _require_int32(q_len=q_len)
     _check_pages(page_table, refs, status, seq_lens)
     B, max_pages = page_table.shape
     page_bytes = _check_page_pool(pool, refs, B, workspace)

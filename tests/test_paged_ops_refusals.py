@@ -183,3 +183,21 @@ def test_pages_binding(lib):
     _refused(m.mla_pages_release, table, lens, refs, match="CUDA tensors")
     _refused(m.mla_pages_compact, pool, table, refs, n_used=torch.zeros(1), match="n_used must be")
     _refused(m.mla_pages_compact, pool, table, refs, match="CUDA tensors")
+
+
+@pytest.mark.parametrize("big", [2**31, 2**32 + 1, -2**31 - 1])
+def test_numbers_past_32_bits(lib, big):
+    """Refused by name, before anything else is looked at: they would wrap to another number."""
+    for name, call in (("window", lambda: m.mla_attend_window_dense(None, None, big)),
+                       ("sinks", lambda: m.mla_attend_window_dense(None, None, 4, big)),
+                       ("window", lambda: m.mla_attend_window_paged(None, None, None, None, big)),
+                       ("sinks", lambda: m.mla_attend_window_paged(None, None, None, None, 4, big)),
+                       ("window", lambda: m.mla_attend_packed(None, None, None, None, window=big)),
+                       ("sinks", lambda: m.mla_attend_packed(None, None, None, None, sinks=big)),
+                       ("q_len", lambda: m.mla_cache_truncate_packed(None, None, None, None, big)),
+                       ("n", lambda: m.mla_cache_unpack(None, None, None, big)),
+                       ("q_len", lambda: m.mla_pages_reserve(None, None, None, None, big)),
+                       ("num_pages", lambda: m.mla_pages_workspace_bytes(1, big)),
+                       ("n", lambda: m.mla_pages_workspace_bytes(big, 1))):
+        with pytest.raises(ValueError, match=f"^{name} must fit 32 bits"):
+            call()
