@@ -8,6 +8,7 @@ not built, importing the binding's functions raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -172,12 +173,24 @@ def _require_int32(**values):
             raise ValueError(f"{name} must fit 32 bits, got {v}")
 
 
-def _used_on(stream, *tensors):
-    """Tells torch's allocator that tensors made here are used on the `stream` of the call."""
+def _allocating_on(stream):
+    """Memory made in this context is the `stream`'s of the call, which uses it first: made on the
+    current stream, it could be memory that kernels pending there still write."""
+    if stream is None:
+        return contextlib.nullcontext()
+    cuda = _get_torch().cuda
+    if stream.device_index != cuda.current_device():
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the current device is cuda:{cuda.current_device()}")
+    return cuda.stream(stream)
+
+
+def _read_here(stream, *tensors):
+    """Tells torch's allocator that results made on `stream` are read on the current stream too."""
     if stream is not None:
+        current = _get_torch().cuda.current_stream()
         for t in tensors:
             if t is not None:
-                t.record_stream(stream)
+                t.record_stream(current)
 
 
 def _require(t, name, dtype, shape=None, min_numel=None, optional=False):
@@ -356,9 +369,10 @@ def mla_attend_window_dense(q_tilde, cache, window, sinks=0, seq_lens=None, scal
     if cache.shape[0] < B:
         raise ValueError(f"cache holds {cache.shape[0]} sequences, q_tilde {B}")
     _check_current(q_tilde, cache, seq_lens, workspace, o_latent, lse, status)
-    workspace = new_workspace(B, Q) if workspace is None else workspace
-    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
-    _used_on(stream, workspace, o_latent, lse)
+    with _allocating_on(stream):
+        workspace = new_workspace(B, Q) if workspace is None else workspace
+        o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
+    _read_here(stream, o_latent, lse)
     _check("mla_attend_window_dense", lib().mla_attend_window_dense(
         _ptr(q_tilde), _ptr(cache), _ptr(seq_lens), B, Q, H, R, cache.shape[1], scale, window, sinks, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _ptr(o_latent), _ptr(lse), _ptr(status), _stream(stream)))
@@ -375,9 +389,10 @@ def mla_attend_window_paged(q_tilde, pool, page_table, seq_lens, window, sinks=0
     if page_table.shape[0] < B:
         raise ValueError(f"page_table has {page_table.shape[0]} rows, q_tilde {B} sequences")
     _check_current(q_tilde, pool, page_table, seq_lens, workspace, o_latent, lse, status)
-    workspace = new_workspace(B, Q) if workspace is None else workspace
-    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
-    _used_on(stream, workspace, o_latent, lse)
+    with _allocating_on(stream):
+        workspace = new_workspace(B, Q) if workspace is None else workspace
+        o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
+    _read_here(stream, o_latent, lse)
     _check("mla_attend_window_paged", lib().mla_attend_window_paged(
         _ptr(q_tilde), _ptr(pool), _ptr(page_table), _ptr(seq_lens), B, Q, H, R, pool.shape[1], page_table.shape[1],
         pool.shape[0], scale, window, sinks, _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -614,9 +629,10 @@ def mla_cache_unpack(pool, page_table, start, n, unit=1.0, rows=None, status=Non
     _check_packed(pool, page_table, B, "start", status)
     _require(rows, "rows", "bf16", (B, n, R), optional=True)
     _check_current(pool, page_table, start, rows, status)
-    if rows is None:
-        rows = torch.empty(B, n, R, dtype=torch.bfloat16, device=pool.device)
-    _used_on(stream, rows)
+    with _allocating_on(stream):
+        if rows is None:
+            rows = torch.empty(B, n, R, dtype=torch.bfloat16, device=pool.device)
+    _read_here(stream, rows)
     _check("mla_cache_unpack", lib().mla_cache_unpack(
         _ptr(pool), _ptr(page_table), _ptr(start), _ptr(rows), B, n, R, PAGE, page_table.shape[1], pool.shape[0],
         unit, _ptr(status), _stream(stream)))
@@ -631,9 +647,10 @@ def mla_attend_packed(q_tilde, pool, page_table, seq_lens, unit=1.0, window=0, s
     B, Q = _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens, seq_lens_required=True)
     _check_packed(pool, page_table, B, "q_tilde", status)
     _check_current(q_tilde, pool, page_table, seq_lens, workspace, o_latent, lse, status)
-    workspace = new_workspace(B, Q) if workspace is None else workspace
-    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
-    _used_on(stream, workspace, o_latent, lse)
+    with _allocating_on(stream):
+        workspace = new_workspace(B, Q) if workspace is None else workspace
+        o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
+    _read_here(stream, o_latent, lse)
     _check("mla_attend_packed", lib().mla_attend_packed(
         _ptr(q_tilde), _ptr(pool), _ptr(page_table), _ptr(seq_lens), B, Q, H, R, PAGE, page_table.shape[1],
         pool.shape[0], unit, window, sinks, scale, _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -680,8 +697,8 @@ def mla_pages_reserve(pool, page_table, seq_lens, refs, q_len, workspace=None, s
     B, max_pages = page_table.shape
     page_bytes = _check_page_pool(pool, refs, B, workspace)
     _check_current(pool, page_table, seq_lens, refs, workspace, status)
-    workspace = new_pages_workspace(B, pool.shape[0]) if workspace is None else workspace
-    _used_on(stream, workspace)
+    with _allocating_on(stream):
+        workspace = new_pages_workspace(B, pool.shape[0]) if workspace is None else workspace
     _check("mla_pages_reserve", lib().mla_pages_reserve(
         _ptr(pool), page_bytes, _ptr(page_table), _ptr(seq_lens), _ptr(refs), B, q_len, max_pages, pool.shape[0],
         _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
@@ -696,8 +713,8 @@ def mla_pages_fork(pool, page_table, seq_lens, refs, parents, children, workspac
     B, max_pages = page_table.shape
     page_bytes = _check_page_pool(pool, refs, n, workspace)
     _check_current(pool, page_table, seq_lens, refs, parents, children, workspace, status)
-    workspace = new_pages_workspace(n, pool.shape[0]) if workspace is None else workspace
-    _used_on(stream, workspace)
+    with _allocating_on(stream):
+        workspace = new_pages_workspace(n, pool.shape[0]) if workspace is None else workspace
     _check("mla_pages_fork", lib().mla_pages_fork(
         _ptr(pool), page_bytes, _ptr(page_table), _ptr(seq_lens), _ptr(refs), _ptr(parents), _ptr(children), n, B,
         max_pages, pool.shape[0], _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
@@ -719,10 +736,11 @@ def mla_pages_compact(pool, page_table, refs, n_used=None, workspace=None, statu
     _require(n_used, "n_used", "i32", min_numel=1, optional=True)
     page_bytes = _check_page_pool(pool, refs, 1, workspace)
     _check_current(pool, page_table, refs, n_used, workspace, status)
-    if n_used is None:
-        n_used = torch.empty(1, dtype=torch.int32, device=pool.device)
-    workspace = new_pages_workspace(1, pool.shape[0]) if workspace is None else workspace
-    _used_on(stream, workspace, n_used)
+    with _allocating_on(stream):
+        if n_used is None:
+            n_used = torch.empty(1, dtype=torch.int32, device=pool.device)
+        workspace = new_pages_workspace(1, pool.shape[0]) if workspace is None else workspace
+    _read_here(stream, n_used)
     _check("mla_pages_compact", lib().mla_pages_compact(
         _ptr(pool), page_bytes, _ptr(page_table), _ptr(refs), page_table.shape[0], page_table.shape[1], pool.shape[0],
         _ptr(n_used), _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))

@@ -177,3 +177,29 @@ def test_stream_argument():
     got = m.mla_attend_packed(qt, c.pool, c.table, c.lens, workspace=ws, stream=s)
     s.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_outputs_of_a_call_on_another_stream_are_not_memory_that_is_still_written():
+    """A tensor of the outputs' size is freed while a copy into it waits on the current stream; a
+    call on another stream makes its outputs meanwhile."""
+    c = Cache(2, 4, 12)
+    c.append(_rows((2, 130), 72))
+    qt = to_dev(synthetic_qtilde(2, 1, seed=73))
+    ws = m.new_workspace(2, 1)
+    want = m.mla_attend_packed(qt, c.pool, c.table, c.lens, workspace=ws)
+    rows = m.mla_cache_unpack(c.pool, c.table, torch.zeros_like(c.lens), 130)
+    torch.cuda.synchronize()
+    start = torch.zeros_like(c.lens)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    gate = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")  # some milliseconds of fills
+    late = [torch.empty_like(x) for x in (*want, rows)]
+    for _ in range(60):
+        gate.zero_()
+    for x in late:
+        x.zero_()
+    del late, x
+    got = m.mla_attend_packed(qt, c.pool, c.table, c.lens, workspace=ws, stream=s)
+    got_rows = m.mla_cache_unpack(c.pool, c.table, start, 130, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got_rows, rows)
