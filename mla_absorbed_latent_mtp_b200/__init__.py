@@ -162,8 +162,9 @@ def _check_cuda(*tensors):
 def _check_current(*tensors):
     """_check_cuda, and that the device is the current one: the kernels are launched there."""
     dev = _check_cuda(*tensors)
-    if dev != _get_torch().cuda.current_device():
-        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{_torch.cuda.current_device()}")
+    current = (_torch or _get_torch()).cuda.current_device()
+    if dev != current:
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{current}")
 
 
 def _require_int32(**values):
@@ -212,7 +213,7 @@ def _require(t, name, dtype, shape=None, min_numel=None, optional=False):
     if shape is not None:
         got = t.shape
         ok = len(got) == len(shape)
-        if ok:
+        if ok and shape != (None, None):
             for g, w in zip(got, shape):
                 if w is not None and g != w:
                     ok = False
@@ -672,22 +673,25 @@ def new_pages_workspace(n: int, num_pages: int):
 def _check_pages(page_table, refs, status, seq_lens=None, lens_required=True):
     _require(page_table, "page_table", "i32", (None, None))
     _require(refs, "refs", "i32", (None,))
-    _require(seq_lens, "seq_lens", "i32", min_numel=page_table.shape[0], optional=not lens_required)
+    if lens_required:
+        _require(seq_lens, "seq_lens", "i32", min_numel=page_table.shape[0])
     _require(status, "status", "i32", min_numel=1, optional=True)
 
 
 def _check_page_pool(pool, refs, n, workspace):
-    """pool [P, 64, ...] of any dtype, contiguous; returns the bytes per page."""
-    if pool is None or not pool.is_contiguous() or pool.dim() < 2 or pool.shape[1] != PAGE:
+    """pool [P, 64, ...] of any dtype, contiguous; returns the bytes per page and P."""
+    shape = () if pool is None else pool.shape
+    if len(shape) < 2 or shape[1] != PAGE or not pool.is_contiguous():
         raise ValueError(f"pool must be a contiguous [P, {PAGE}, ...] tensor")
-    P = int(pool.shape[0])
+    P = shape[0]
     if refs.numel() != P:
         raise ValueError(f"refs must have one element per page ({P}), got {refs.numel()}")
     if workspace is not None:
-        _require(workspace, "workspace", "u8", min_numel=mla_pages_workspace_bytes(n, P))
+        _require(workspace, "workspace", "u8", min_numel=lib().mla_pages_workspace_bytes(n, P))
     page_bytes = pool.numel() * pool.element_size() // max(P, 1)
-    _require_int32(page_bytes=page_bytes)
-    return page_bytes
+    if page_bytes >= 2**31:
+        raise ValueError(f"pages of {page_bytes} bytes")
+    return page_bytes, P
 
 
 def mla_pages_reserve(pool, page_table, seq_lens, refs, q_len, workspace=None, status=None, stream=None):
@@ -695,12 +699,13 @@ def mla_pages_reserve(pool, page_table, seq_lens, refs, q_len, workspace=None, s
     _require_int32(q_len=q_len)
     _check_pages(page_table, refs, status, seq_lens)
     B, max_pages = page_table.shape
-    page_bytes = _check_page_pool(pool, refs, B, workspace)
+    page_bytes, P = _check_page_pool(pool, refs, B, workspace)
     _check_current(pool, page_table, seq_lens, refs, workspace, status)
-    with _allocating_on(stream):
-        workspace = new_pages_workspace(B, pool.shape[0]) if workspace is None else workspace
+    if workspace is None:
+        with _allocating_on(stream):
+            workspace = new_pages_workspace(B, P)
     _check("mla_pages_reserve", lib().mla_pages_reserve(
-        _ptr(pool), page_bytes, _ptr(page_table), _ptr(seq_lens), _ptr(refs), B, q_len, max_pages, pool.shape[0],
+        _ptr(pool), page_bytes, _ptr(page_table), _ptr(seq_lens), _ptr(refs), B, q_len, max_pages, P,
         _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
 
 
@@ -711,21 +716,23 @@ def mla_pages_fork(pool, page_table, seq_lens, refs, parents, children, workspac
     n = parents.shape[0]
     _require(children, "children", "i32", (n,))
     B, max_pages = page_table.shape
-    page_bytes = _check_page_pool(pool, refs, n, workspace)
+    page_bytes, P = _check_page_pool(pool, refs, n, workspace)
     _check_current(pool, page_table, seq_lens, refs, parents, children, workspace, status)
-    with _allocating_on(stream):
-        workspace = new_pages_workspace(n, pool.shape[0]) if workspace is None else workspace
+    if workspace is None:
+        with _allocating_on(stream):
+            workspace = new_pages_workspace(n, P)
     _check("mla_pages_fork", lib().mla_pages_fork(
         _ptr(pool), page_bytes, _ptr(page_table), _ptr(seq_lens), _ptr(refs), _ptr(parents), _ptr(children), n, B,
-        max_pages, pool.shape[0], _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
+        max_pages, P, _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
 
 
 def mla_pages_release(page_table, seq_lens, refs, status=None, stream=None):
     """Unmap the entries behind each sequence's last row (all of them where its length is 0)."""
     _check_pages(page_table, refs, status, seq_lens)
     _check_current(page_table, seq_lens, refs, status)
+    B, max_pages = page_table.shape
     _check("mla_pages_release", lib().mla_pages_release(
-        _ptr(page_table), _ptr(seq_lens), _ptr(refs), page_table.shape[0], page_table.shape[1], refs.numel(),
+        _ptr(page_table), _ptr(seq_lens), _ptr(refs), B, max_pages, refs.numel(),
         _ptr(status), _stream(stream)))
 
 
@@ -734,15 +741,15 @@ def mla_pages_compact(pool, page_table, refs, n_used=None, workspace=None, statu
     torch = _get_torch()
     _check_pages(page_table, refs, status, lens_required=False)
     _require(n_used, "n_used", "i32", min_numel=1, optional=True)
-    page_bytes = _check_page_pool(pool, refs, 1, workspace)
+    page_bytes, P = _check_page_pool(pool, refs, 1, workspace)
     _check_current(pool, page_table, refs, n_used, workspace, status)
     with _allocating_on(stream):
         if n_used is None:
             n_used = torch.empty(1, dtype=torch.int32, device=pool.device)
-        workspace = new_pages_workspace(1, pool.shape[0]) if workspace is None else workspace
+        workspace = new_pages_workspace(1, P) if workspace is None else workspace
     _read_here(stream, n_used)
     _check("mla_pages_compact", lib().mla_pages_compact(
-        _ptr(pool), page_bytes, _ptr(page_table), _ptr(refs), page_table.shape[0], page_table.shape[1], pool.shape[0],
+        _ptr(pool), page_bytes, _ptr(page_table), _ptr(refs), page_table.shape[0], page_table.shape[1], P,
         _ptr(n_used), _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
     return n_used
 
