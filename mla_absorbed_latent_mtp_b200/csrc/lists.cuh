@@ -161,10 +161,10 @@ __device__ __forceinline__ void report_length(const P &p, int b) {
 }
 
 template <class Order>
-__device__ __forceinline__ void row_to_shared(uint16_t *row, const float4 &o, float inv, int t) {
+__device__ __forceinline__ void row_to_shared(uint16_t *row, const float4 &o, float inv, int at) {
   const float v[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) row[Order::latent(4 * t + e)] = (uint16_t)(pack_bf16x2(v[e], 0.f) & 0xFFFFu);
+  for (int e = 0; e < 4; ++e) row[Order::latent(at + e)] = (uint16_t)(pack_bf16x2(v[e], 0.f) & 0xFFFFu);
 }
 template <class P>
 __device__ __forceinline__ void write_row(const P &p, long long at, const uint16_t *row, float M,
@@ -174,35 +174,37 @@ __device__ __forceinline__ void write_row(const P &p, long long at, const uint16
     p.lse[at] = M == -INFINITY ? -INFINITY : (M + log2f(den)) * 0.69314718055994530942f;
 }
 
-// Many query rows, few partials each: a block takes two heads of a row and merges online, three
-// partials at a time, all their loads in flight at once.
-constexpr int kFewHeads = 2, kFewChunk = 3;
-template <class Seqs, class Order, class P>
+// Many query rows, few partials each: a block takes some heads of a row and merges online, some
+// partials at a time, all their loads in flight at once: two heads and three partials, or, with at
+// least as many sequences as groups (where most rows have one or two partials, and blocks come in
+// waves), four heads and one (4-bit rows, 148 x 100: the call 30.5 us with two heads, 28.9 with
+// four, 33.8 with eight; but 32 x 1,024: 25.6 with two, 28.9 with four).
+template <int kH, int kChunk, class Seqs, class Order, class P>
 __global__ void __launch_bounds__(128, 8) combine_few_kernel(const P p, float unit) {
   grid_dep_launch();
   grid_dep_wait();
   const int v = blockIdx.x, b = v / p.Q, i = v % p.Q, t = threadIdx.x;
-  const int h0 = blockIdx.y * kFewHeads;
-  __shared__ __align__(16) uint16_t row[kFewHeads][kLatent];
+  const int h0 = blockIdx.y * kH;
+  __shared__ __align__(16) uint16_t row[kH][kLatent];
   const Partials pt(p, b);
   if (t == 0 && blockIdx.y == 0 && i == 0) report_length<Seqs>(p, b);
-  float M[kFewHeads], den[kFewHeads];
-  float4 acc[kFewHeads];
+  float M[kH], den[kH];
+  float4 acc[kH];
 #pragma unroll
-  for (int hh = 0; hh < kFewHeads; ++hh) {
+  for (int hh = 0; hh < kH; ++hh) {
     M[hh] = -INFINITY;
     den[hh] = 0.f;
     acc[hh] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  for (int k0 = 0; k0 < pt.count; k0 += kFewChunk) {
-    float mk[kFewHeads][kFewChunk], lk[kFewHeads][kFewChunk];
-    float4 ok[kFewHeads][kFewChunk];
+  for (int k0 = 0; k0 < pt.count; k0 += kChunk) {
+    float mk[kH][kChunk], lk[kH][kChunk];
+    float4 ok[kH][kChunk];
 #pragma unroll
-    for (int j = 0; j < kFewChunk; ++j) {
+    for (int j = 0; j < kChunk; ++j) {
       const bool live = k0 + j < pt.count;
       const long long slot = live ? pt.slot(p, k0 + j, b, i) : 0;
 #pragma unroll
-      for (int hh = 0; hh < kFewHeads; ++hh) {
+      for (int hh = 0; hh < kH; ++hh) {
         const long long r = slot * kHeads + h0 + hh;
         mk[hh][j] = live ? p.part_m[r] : -INFINITY;
         lk[hh][j] = live ? p.part_l[r] : 0.f;
@@ -211,10 +213,10 @@ __global__ void __launch_bounds__(128, 8) combine_few_kernel(const P p, float un
       }
     }
 #pragma unroll
-    for (int hh = 0; hh < kFewHeads; ++hh) {
+    for (int hh = 0; hh < kH; ++hh) {
       float mx = M[hh];
 #pragma unroll
-      for (int j = 0; j < kFewChunk; ++j) mx = fmaxf(mx, mk[hh][j]);
+      for (int j = 0; j < kChunk; ++j) mx = fmaxf(mx, mk[hh][j]);
       if (mx == -INFINITY) continue;
       const float a = exp2f(M[hh] - mx);  // 0 when M was -inf
       den[hh] *= a;
@@ -223,7 +225,7 @@ __global__ void __launch_bounds__(128, 8) combine_few_kernel(const P p, float un
       acc[hh].z *= a;
       acc[hh].w *= a;
 #pragma unroll
-      for (int j = 0; j < kFewChunk; ++j) {
+      for (int j = 0; j < kChunk; ++j) {
         if (mk[hh][j] == -INFINITY) continue;  // an empty partial's O was never written
         const float w = exp2f(mk[hh][j] - mx);
         den[hh] += w * lk[hh][j];
@@ -236,16 +238,17 @@ __global__ void __launch_bounds__(128, 8) combine_few_kernel(const P p, float un
     }
   }
 #pragma unroll
-  for (int hh = 0; hh < kFewHeads; ++hh)
-    row_to_shared<Order>(row[hh], acc[hh], M[hh] == -INFINITY ? 0.f : unit / den[hh], t);
+  for (int hh = 0; hh < kH; ++hh)
+    row_to_shared<Order>(row[hh], acc[hh], M[hh] == -INFINITY ? 0.f : unit / den[hh], 4 * t);
   __syncthreads();
 #pragma unroll
-  for (int hh = 0; hh < kFewHeads; ++hh) write_row(p, (long long)v * kHeads + h0 + hh, row[hh], M[hh], den[hh], t);
+  for (int hh = 0; hh < kH; ++hh) write_row(p, (long long)v * kHeads + h0 + hh, row[hh], M[hh], den[hh], t);
 }
 
 // Few sequences, many partials each: a block takes one head of a row; eight slices of 128 threads
 // take every eighth partial, all of a thread's loads independent, and are added up in order (1 x
-// 8,192 rows, 64 partials: the call 66.6 us with the kernel above, 23.9 with this one).
+// 8,192 rows, 64 partials: the call 66.6 us with the kernel above, 23.9 with this one; 4 x 8,192
+// rows: 48.3 and 26.1).
 constexpr int kSlices = 8;
 constexpr int kMaxPartials = 256;  // per sequence: at most one per CTA group
 template <class Seqs, class Order, class P>
@@ -304,19 +307,117 @@ __global__ void __launch_bounds__(128 * kSlices) combine_many_kernel(const P p, 
       acc.z += o.z;
       acc.w += o.w;
     }
-    row_to_shared<Order>(row, acc, top == -INFINITY ? 0.f : unit / total, t);
+    row_to_shared<Order>(row, acc, top == -INFINITY ? 0.f : unit / total, 4 * t);
   }
   __syncthreads();
   if (slice == 0) write_row(p, (long long)v * kHeads + h, row, top, total, t);
 }
 
+// A single query row: its 64 heads alone are too few blocks to read the partials at speed, so four
+// blocks take a quarter of a head's latents each, a warp per slice; the weights' loads are in flight
+// at once, and the first partials' before the weights are known.  (1 x 18,944 rows, 148 partials:
+// the call 28.9 us with the kernel above, 22.9 with this one; with two rows that one is as fast,
+// and with four this one's registers cost more than its blocks give: 26.0 us against 30.0.)
+constexpr int kRowParts = 4, kRowThreads = 512;
+template <class Seqs, class Order, class P>
+__global__ void __launch_bounds__(kRowThreads) combine_row_kernel(const P p, float unit) {
+  constexpr int kLanes = 128 / kRowParts, kSlices = kRowThreads / kLanes, kAhead = 4;
+  grid_dep_launch();
+  grid_dep_wait();
+  const int b = 0, i = 0, h = blockIdx.x, part = blockIdx.y;
+  const int t = threadIdx.x % kLanes, slice = threadIdx.x / kLanes, lane = threadIdx.x % 32;
+  __shared__ float weight[kMaxPartials];
+  __shared__ float4 sum[kSlices][kLanes];
+  __shared__ __align__(16) uint16_t row[kLatent];
+  __shared__ float total, top;
+  const Partials pt(p, b);
+  const int at = Order::unit(part, t);  // the first of this thread's four stored values
+  float4 first[kAhead];
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    const int k = slice + j * kSlices;
+    first[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (k < pt.count)
+      first[j] = *reinterpret_cast<const float4 *>(p.part_o + (pt.slot(p, k, b, i) * kHeads + h) * kLatent + at);
+  }
+  if (threadIdx.x == 0 && h == 0 && part == 0) report_length<Seqs>(p, b);
+  if (threadIdx.x < 32) {
+    float m[kMaxPartials / 32], l[kMaxPartials / 32], M = -INFINITY, den = 0.f;
+#pragma unroll
+    for (int j = 0; j < kMaxPartials / 32; ++j) {
+      const int k = lane + 32 * j;
+      m[j] = -INFINITY;
+      l[j] = 0.f;
+      if (k < pt.count) {
+        const long long r = pt.slot(p, k, b, i) * kHeads + h;
+        m[j] = p.part_m[r];
+        l[j] = p.part_l[r];
+      }
+      M = fmaxf(M, m[j]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll
+    for (int j = 0; j < kMaxPartials / 32; ++j) {
+      const int k = lane + 32 * j;
+      const float w = m[j] == -INFINITY ? 0.f : exp2f(m[j] - M);  // an empty partial's O was never written
+      if (k < pt.count) weight[k] = w;
+      den += w * l[j];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    if (lane == 0) {
+      total = den;
+      top = M;
+    }
+  }
+  __syncthreads();
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float w, const float4 &o) {
+    if (w == 0.f) return;
+    acc.x += w * o.x;
+    acc.y += w * o.y;
+    acc.z += w * o.z;
+    acc.w += w * o.w;
+  };
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) {
+    const int k = slice + j * kSlices;
+    if (k < pt.count) add(weight[k], first[j]);
+  }
+#pragma unroll 4
+  for (int k = slice + kAhead * kSlices; k < pt.count; k += kSlices)
+    add(weight[k], *reinterpret_cast<const float4 *>(p.part_o + (pt.slot(p, k, b, i) * kHeads + h) * kLatent + at));
+  sum[slice][t] = acc;
+  __syncthreads();
+  if (slice == 0) {
+    for (int s = 1; s < kSlices; ++s) {
+      const float4 o = sum[s][t];
+      acc.x += o.x;
+      acc.y += o.y;
+      acc.z += o.z;
+      acc.w += o.w;
+    }
+    row_to_shared<Order>(row, acc, top == -INFINITY ? 0.f : unit / total, at);
+  }
+  __syncthreads();
+  if (slice == 0) write_row(p, h, row, top, total, part * kLanes + t);  // the part's latents are adjacent
+}
+
 template <class Seqs, class Order, class P>
 cudaError_t launch_combine(const P &p, float unit, cudaStream_t stream) {
+  const int rows = p.B * p.Q;
+  if (rows == 1)
+    return launch_chained(combine_row_kernel<Seqs, Order, P>, dim3(kHeads, kRowParts), dim3(kRowThreads), 0, stream, p,
+                          unit);
   if (p.B <= p.groups / 16)  // sixteen partials a sequence or more
-    return launch_chained(combine_many_kernel<Seqs, Order, P>, dim3(p.B * p.Q, kHeads), dim3(128 * kSlices), 0, stream,
-                          p, unit);
-  return launch_chained(combine_few_kernel<Seqs, Order, P>, dim3(p.B * p.Q, kHeads / kFewHeads), dim3(128), 0, stream,
-                        p, unit);
+    return launch_chained(combine_many_kernel<Seqs, Order, P>, dim3(rows, kHeads), dim3(128 * kSlices), 0, stream, p,
+                          unit);
+  if (p.B >= p.groups)  // two partials a sequence or fewer, on average
+    return launch_chained(combine_few_kernel<4, 1, Seqs, Order, P>, dim3(rows, kHeads / 4), dim3(128), 0, stream, p,
+                          unit);
+  return launch_chained(combine_few_kernel<2, 3, Seqs, Order, P>, dim3(rows, kHeads / 2), dim3(128), 0, stream, p,
+                        unit);
 }
 
 }  // namespace lists

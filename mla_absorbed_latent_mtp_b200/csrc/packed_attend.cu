@@ -95,6 +95,8 @@ struct PartialOrder {
     const int mb = idx / 128, L = idx % 128;
     return kGroup * (8 * (L / 32) + L % 8) + 4 * mb + L % 32 / 8;
   }
+  // Stored place of the first of four values of thread t (of 32) in quarter `part` of the latents.
+  static __device__ __forceinline__ int unit(int part, int t) { return 128 * (t / 8) + 32 * part + 4 * (t % 8); }
 };
 
 // Instruction descriptor, kind::f16 with fp16 A and B and fp32 D.

@@ -133,6 +133,8 @@ struct SegIter {
 
 struct PartialOrder {  // partials are stored latent by latent
   static __device__ __forceinline__ int latent(int idx) { return idx; }
+  // The first of four values of thread t (of 32) in quarter `part` of the latents.
+  static __device__ __forceinline__ int unit(int part, int t) { return 128 * part + 4 * t; }
 };
 
 // ------------------------------------------------------------------ shared state

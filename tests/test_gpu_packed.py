@@ -271,3 +271,28 @@ def test_attend_many_queries_and_many_sequences():
         torch.cuda.synchronize()
         assert int(st.item()) == 0
         _check(lens, values, qt, window, sinks, o, lse)
+
+
+# a single row, some sequences with many partials, with few, and more sequences than CTA groups
+MERGES = [(1, [0]), (1, [1]), (1, [300]), (1, [18944]), (1, [20001]), (2, [5000]), (6, [4100]), (1, [8000, 37]), (1, [0, 6000, 3]),
+          (1, [700] * 9), (1, [1200 + 77 * k for k in range(12)]), (8, [118] * 25), (8, [9 + 13 * k for k in range(20)]),
+          (1, [100] * 148), (1, [k % 5 * 130 for k in range(160)])]
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (200, 5)])
+@pytest.mark.parametrize("q_len,lens", MERGES, ids=[f"{len(x)}x{q}x{max(x)}" for q, x in MERGES])
+def test_merges_read_only_what_the_call_wrote(q_len, lens, window, sinks):
+    """The workspace holds NaN before the call; twice, with the first call's contents before the second."""
+    room = 0 if max(lens) else 1  # a pool and a table have at least one page (no pages: MLA_ERR_ARG)
+    lens, table, pool, values = _setup(lens, room, seed=31)
+    qt = synthetic_qtilde(len(lens), q_len, seed=32)
+    ws = m.new_workspace(len(lens), q_len)
+    ws.fill_(0xFF)
+    st = _status()
+    args = (to_dev(qt), torch.from_numpy(pool).cuda(), ints_to_dev(table), ints_to_dev(lens))
+    o, lse = m.mla_attend_packed(*args, window=window, sinks=sinks, workspace=ws, status=st)
+    again, lse_again = m.mla_attend_packed(*args, window=window, sinks=sinks, workspace=ws, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert torch.equal(o, again) and torch.equal(lse, lse_again)
+    _check(lens, values, qt, window, sinks, o, lse)

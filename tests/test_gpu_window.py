@@ -166,3 +166,23 @@ def test_bad_pages_and_lengths_are_flagged():
     m.mla_attend_window_paged(qt, pool, ints_to_dev(table), ints_to_dev([200, 4 * PAGE + 1]), 100, 3, status=st)
     torch.cuda.synchronize()
     assert int(st.item()) == m.MLA_ERR_INDEX
+
+
+@pytest.mark.parametrize("q_len,lens,window,sinks", [(1, [1], 1, 0), (1, [12000], 20000, 0), (1, [12000], 3000, 70), (6, [2500], 900, 3),
+                                                     (1, [700] * 9, 800, 0), (8, [118] * 25, 50, 4), (1, [100] * 148, 70, 0),
+                                                     (1, [k % 5 * 70 for k in range(160)], 100, 1)])
+def test_merges_read_only_what_the_call_wrote(q_len, lens, window, sinks):
+    """The workspace holds NaN before the call; twice, with the first call's contents before the second."""
+    lens = np.array(lens, dtype=np.int32)
+    bits = synth.normal_bf16((len(lens), max(int(lens.max()), 1), R), 33, synth.STREAM_CACHE)
+    qt = synthetic_qtilde(len(lens), q_len, seed=34)
+    ws = m.new_workspace(len(lens), q_len)
+    ws.fill_(0xFF)
+    st = _status()
+    args = (to_dev(qt), to_dev(bits), window, sinks, ints_to_dev(lens))
+    o, lse = m.mla_attend_window_dense(*args, workspace=ws, status=st)
+    again, lse_again = m.mla_attend_window_dense(*args, workspace=ws, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert torch.equal(o, again) and torch.equal(lse, lse_again)
+    _check(lens, oracle.widen(bits), qt, window, sinks, o, lse)
