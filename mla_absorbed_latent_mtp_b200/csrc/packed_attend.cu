@@ -13,8 +13,8 @@
 // operand is unpacked into TENSOR memory, twice, by register, and shared memory holds only the
 // packed rows, q~ and P.  Measured: 5,300 cycles a tile, 2.6 times the MMAs' own; the rest is the
 // unpacking, the softmax and the hand-overs between them (3,070 instructions a tile and scheduler).
-// With the merge 32 x 8,192 rows take 67 us, 16 sequences of 1.05 M rows in all 192 us, 16 x 6
-// queries with a window of 8,191 rows and 64 sinks 144 us.
+// With the merge 32 x 8,192 rows take 67 us, 16 sequences of 1.05 M rows in all 193 us (217 in a
+// long run), 16 x 6 queries with a window of 8,191 rows and 64 sinks 145 to 148 us (152).
 //   S^T[rows, heads]    = C (A: 128 rows on the lanes, 64 latents a chunk) * Q~^T (smem)
 //   O^T[latent, heads] += C^T (A: 128 latents on the lanes, 16 rows a chunk, x 4) * P^T (smem)
 // Both unpackings read the same packed words.  For C a thread owns a row.  For C^T a thread
@@ -646,8 +646,8 @@ __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint
     }
     // The last segment's scores are done: this one's q~ takes the place of that one's before its
     // O^T is stored, so that the first scores are computed meanwhile (256 x 500 rows: 80.0 us with
-    // the store first, 74.9 so; 32 x 8,192: 68.1, 67.5; 16 x 6 queries, window 8,191 + 64, two draws of
-    // the lengths: 142.2 and 145.1, 144.9 and 144.7).
+    // the store first, 74.9 so; 32 x 8,192: 69.7, 69.2; against it 16 ragged sequences, 214 and 217,
+    // and 16 x 6 queries, window 8,191 + 64, 149 and 152: the loop over tiles is compiled a little worse).
     if (more) convert_query(p, sh, sg.b, iq, w, lane);
     if (slot >= 0) {
       wait(bar, kBarOFull, segs & 1);

@@ -434,7 +434,7 @@ __device__ void softmax_role(const WindowParams &p, const Shared &sh, uint32_t t
             m_reg[2 * j + e] = m_used[c];
           }
       }
-      // probabilities, rounded to bf16 for the value product; l sums the rounded values.
+      // probabilities, rounded to bf16 for the value product.
       // They are computed into registers first: the wait for this P buffer (the value
       // product of tile n-2) then overlaps the exponentials instead of preceding them.
       uint32_t pw[8];
@@ -527,7 +527,7 @@ __device__ void softmax_role(const WindowParams &p, const Shared &sh, uint32_t t
 template <bool kPaged>
 // Bounds for 384 threads: eleven warps put three on some SM sub-partitions, whose 16K
 // registers then cap a thread at 168 (the 352-thread bound alone would allow 184).
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     attend_window_kernel(const __grid_constant__ CUtensorMap tm_cache, const __grid_constant__ CUtensorMap tm_qt,
                          const WindowParams p) {
   extern __shared__ uint8_t smem_raw[];
