@@ -5,6 +5,10 @@ Tensors are torch CUDA tensors (bf16 as torch.bfloat16, int32 as torch.int32); t
 functions pass their device pointers and the current CUDA stream to the C ABI and
 raise MLAError on a non-zero status.  There is no CPU fallback: if the library is
 not built, importing the binding's functions raises.
+
+A call with stream=s runs on s.  What it allocates (results, workspace, the intermediates of
+mla_decode) is memory of s, and its results may be read on the current stream once that waits
+for s.  Its arguments are the caller's to order before the call and to keep until s has read them.
 """
 from __future__ import annotations
 
@@ -176,7 +180,8 @@ def _require_int32(**values):
 
 def _allocating_on(stream):
     """Memory made in this context is the `stream`'s of the call, which uses it first: made on the
-    current stream, it could be memory that kernels pending there still write."""
+    current stream, it could be memory that kernels pending there still write, and, dropped when
+    the call returns, memory that the next tensor there is given while `stream` still reads it."""
     if stream is None:
         return contextlib.nullcontext()
     cuda = _get_torch().cuda
@@ -192,6 +197,17 @@ def _read_here(stream, *tensors):
         for t in tensors:
             if t is not None:
                 t.record_stream(current)
+
+
+def _new(stream, shape, dtype, device, make=None):
+    """A result of a call on `stream`."""
+    make = make or _get_torch().empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with _allocating_on(stream):
+        t = make(shape, dtype=dtype, device=device)
+    _read_here(stream, t)
+    return t
 
 
 def _require(t, name, dtype, shape=None, min_numel=None, optional=False):
@@ -230,11 +246,12 @@ def mla_attend_workspace_bytes(B: int, Q: int, heads: int = H, latent: int = R) 
     return int(lib().mla_attend_workspace_bytes(B, Q, heads, latent))
 
 
-def new_workspace(B: int, Q: int):
-    """Allocate (with torch) the workspace the attend calls need."""
+def new_workspace(B: int, Q: int, stream=None):
+    """Allocate (with torch) the workspace the attend calls need, on `stream` if it is given."""
     torch = _get_torch()
     n = mla_attend_workspace_bytes(B, Q)
-    return torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+    with _allocating_on(stream):
+        return torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
 
 
 def mla_absorb_q(q, w_uk, q_tilde=None, stream=None):
@@ -248,7 +265,7 @@ def mla_absorb_q(q, w_uk, q_tilde=None, stream=None):
     _require(q_tilde, "q_tilde", "bf16", tuple(q.shape[:-1]) + (R,), optional=True)
     _check_cuda(q, w_uk, q_tilde)
     if q_tilde is None:
-        q_tilde = torch.empty(*q.shape[:-1], R, dtype=torch.bfloat16, device=q.device)
+        q_tilde = _new(stream, tuple(q.shape[:-1]) + (R,), torch.bfloat16, q.device)
     _check("mla_absorb_q", lib().mla_absorb_q(_ptr(q), _ptr(w_uk), _ptr(q_tilde), n, H, D, R, _stream(stream)))
     return q_tilde
 
@@ -264,7 +281,7 @@ def mla_up_proj(o_latent, w_uv, out=None, stream=None):
     _require(out, "out", "bf16", tuple(o_latent.shape[:-1]) + (D,), optional=True)
     _check_cuda(o_latent, w_uv, out)
     if out is None:
-        out = torch.empty(*o_latent.shape[:-1], D, dtype=torch.bfloat16, device=o_latent.device)
+        out = _new(stream, tuple(o_latent.shape[:-1]) + (D,), torch.bfloat16, o_latent.device)
     _check("mla_up_proj", lib().mla_up_proj(_ptr(o_latent), _ptr(w_uv), _ptr(out), n, H, D, R, _stream(stream)))
     return out
 
@@ -282,13 +299,13 @@ def _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens, seq_lens_
     return B, Q
 
 
-def _attend_outputs(q_tilde, o_latent, lse, want_lse):
+def _attend_outputs(q_tilde, o_latent, lse, want_lse, stream=None):
     torch = _get_torch()
     B, Q = q_tilde.shape[0], q_tilde.shape[1]
     if o_latent is None:
-        o_latent = torch.empty(B, Q, H, R, dtype=torch.bfloat16, device=q_tilde.device)
+        o_latent = _new(stream, (B, Q, H, R), torch.bfloat16, q_tilde.device)
     if lse is None and want_lse:
-        lse = torch.empty(B, Q, H, dtype=torch.float32, device=q_tilde.device)
+        lse = _new(stream, (B, Q, H), torch.float32, q_tilde.device)
     return o_latent, lse
 
 
@@ -301,8 +318,8 @@ def mla_attend_dense(q_tilde, cache, seq_lens=None, scale=SCALE, workspace=None,
         raise ValueError(f"cache holds {cache.shape[0]} sequences, q_tilde {B}")
     _check_cuda(q_tilde, cache, seq_lens, workspace, o_latent, lse, status)
     Lmax = cache.shape[1]
-    workspace = new_workspace(B, Q) if workspace is None else workspace
-    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
+    workspace = new_workspace(B, Q, stream) if workspace is None else workspace
+    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse, stream)
     _check("mla_attend_dense", lib().mla_attend_dense(
         _ptr(q_tilde), _ptr(cache), _ptr(seq_lens), B, Q, H, R, Lmax, scale, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _ptr(o_latent), _ptr(lse), _ptr(status), _stream(stream)))
@@ -318,7 +335,7 @@ def mla_attend_dense_noalloc(q_tilde, cache, seq_lens=None, scale=SCALE, o_laten
     if cache.shape[0] < B:
         raise ValueError(f"cache holds {cache.shape[0]} sequences, q_tilde {B}")
     _check_cuda(q_tilde, cache, seq_lens, o_latent, lse, status)
-    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
+    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse, stream)
     _check("mla_attend_dense_noalloc", lib().mla_attend_dense_noalloc(
         _ptr(q_tilde), _ptr(cache), _ptr(seq_lens), B, Q, H, R, cache.shape[1], scale, _ptr(o_latent), _ptr(lse),
         _ptr(status), _stream(stream)))
@@ -334,8 +351,8 @@ def mla_attend_paged(q_tilde, pool, page_table, seq_lens, scale=SCALE, workspace
     if page_table.shape[0] < B:
         raise ValueError(f"page_table has {page_table.shape[0]} rows, q_tilde {B} sequences")
     _check_cuda(q_tilde, pool, page_table, seq_lens, workspace, o_latent, lse, status)
-    workspace = new_workspace(B, Q) if workspace is None else workspace
-    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
+    workspace = new_workspace(B, Q, stream) if workspace is None else workspace
+    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse, stream)
     _check("mla_attend_paged", lib().mla_attend_paged(
         _ptr(q_tilde), _ptr(pool), _ptr(page_table), _ptr(seq_lens), B, Q, H, R, pool.shape[1],
         page_table.shape[1], pool.shape[0], scale, _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -352,8 +369,8 @@ def mla_attend_indexed(q_tilde, cache, indices, seq_lens=None, scale=SCALE, work
         raise ValueError(f"cache holds {cache.shape[0]} sequences, q_tilde {B}")
     _require(indices, "indices", "i32", (B, Q, None))
     _check_cuda(q_tilde, cache, indices, seq_lens, workspace, o_latent, lse, status)
-    workspace = new_workspace(B, Q) if workspace is None else workspace
-    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
+    workspace = new_workspace(B, Q, stream) if workspace is None else workspace
+    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse, stream)
     _check("mla_attend_indexed", lib().mla_attend_indexed(
         _ptr(q_tilde), _ptr(cache), _ptr(indices), _ptr(seq_lens), B, Q, H, R, cache.shape[1], indices.shape[2],
         scale, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(o_latent), _ptr(lse),
@@ -401,15 +418,15 @@ def mla_attend_window_paged(q_tilde, pool, page_table, seq_lens, window, sinks=0
     return o_latent, lse
 
 
-def _fused_outputs(q_tilde, w_uv, out, o_latent, lse, want_lse):
+def _fused_outputs(q_tilde, w_uv, out, o_latent, lse, want_lse, stream):
     torch = _get_torch()
     B, Q = q_tilde.shape[0], q_tilde.shape[1]
     _require(w_uv, "w_uv", "bf16", (H, D, R))
     _require(out, "out", "bf16", (B, Q, H, D), optional=True)
     if out is None:
-        out = torch.empty(B, Q, H, D, dtype=torch.bfloat16, device=q_tilde.device)
+        out = _new(stream, (B, Q, H, D), torch.bfloat16, q_tilde.device)
     if lse is None and want_lse:
-        lse = torch.empty(B, Q, H, dtype=torch.float32, device=q_tilde.device)
+        lse = _new(stream, (B, Q, H), torch.float32, q_tilde.device)
     return out, lse
 
 
@@ -422,9 +439,9 @@ def mla_attend_up_dense(q_tilde, cache, w_uv, seq_lens=None, scale=SCALE, worksp
     _require(cache, "cache", "bf16", (None, None, R))
     if cache.shape[0] < B:
         raise ValueError(f"cache holds {cache.shape[0]} sequences, q_tilde {B}")
-    out, lse = _fused_outputs(q_tilde, w_uv, out, o_latent, lse, want_lse)
+    out, lse = _fused_outputs(q_tilde, w_uv, out, o_latent, lse, want_lse, stream)
     _check_cuda(q_tilde, cache, w_uv, seq_lens, workspace, out, o_latent, lse, status)
-    workspace = new_workspace(B, Q) if workspace is None else workspace
+    workspace = new_workspace(B, Q, stream) if workspace is None else workspace
     _check("mla_attend_up_dense", lib().mla_attend_up_dense(
         _ptr(q_tilde), _ptr(cache), _ptr(seq_lens), B, Q, H, R, cache.shape[1], scale, _ptr(w_uv), D,
         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out), _ptr(o_latent), _ptr(lse),
@@ -440,9 +457,9 @@ def mla_attend_up_paged(q_tilde, pool, page_table, seq_lens, w_uv, scale=SCALE, 
     _require(page_table, "page_table", "i32", (None, None))
     if page_table.shape[0] < B:
         raise ValueError(f"page_table has {page_table.shape[0]} rows, q_tilde {B} sequences")
-    out, lse = _fused_outputs(q_tilde, w_uv, out, o_latent, lse, want_lse)
+    out, lse = _fused_outputs(q_tilde, w_uv, out, o_latent, lse, want_lse, stream)
     _check_cuda(q_tilde, pool, page_table, seq_lens, w_uv, workspace, out, o_latent, lse, status)
-    workspace = new_workspace(B, Q) if workspace is None else workspace
+    workspace = new_workspace(B, Q, stream) if workspace is None else workspace
     _check("mla_attend_up_paged", lib().mla_attend_up_paged(
         _ptr(q_tilde), _ptr(pool), _ptr(page_table), _ptr(seq_lens), B, Q, H, R, pool.shape[1], page_table.shape[1],
         pool.shape[0], scale, _ptr(w_uv), D, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out),
@@ -458,9 +475,9 @@ def mla_attend_up_indexed(q_tilde, cache, indices, w_uv, seq_lens=None, scale=SC
     if cache.shape[0] < B:
         raise ValueError(f"cache holds {cache.shape[0]} sequences, q_tilde {B}")
     _require(indices, "indices", "i32", (B, Q, None))
-    out, lse = _fused_outputs(q_tilde, w_uv, out, o_latent, lse, want_lse)
+    out, lse = _fused_outputs(q_tilde, w_uv, out, o_latent, lse, want_lse, stream)
     _check_cuda(q_tilde, cache, indices, w_uv, seq_lens, workspace, out, o_latent, lse, status)
-    workspace = new_workspace(B, Q) if workspace is None else workspace
+    workspace = new_workspace(B, Q, stream) if workspace is None else workspace
     _check("mla_attend_up_indexed", lib().mla_attend_up_indexed(
         _ptr(q_tilde), _ptr(cache), _ptr(indices), _ptr(seq_lens), B, Q, H, R, cache.shape[1], indices.shape[2],
         scale, _ptr(w_uv), D, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out),
@@ -481,8 +498,8 @@ def mla_expand_kv(c, w_uk, w_uv, k=None, v=None, stream=None):
     _require(k, "k", "bf16", shape, optional=True)
     _require(v, "v", "bf16", shape, optional=True)
     _check_cuda(c, w_uk, w_uv, k, v)
-    k = torch.empty(shape, dtype=torch.bfloat16, device=c.device) if k is None else k
-    v = torch.empty(shape, dtype=torch.bfloat16, device=c.device) if v is None else v
+    k = _new(stream, shape, torch.bfloat16, c.device) if k is None else k
+    v = _new(stream, shape, torch.bfloat16, c.device) if v is None else v
     _check("mla_expand_kv", lib().mla_expand_kv(_ptr(c), _ptr(w_uk), _ptr(w_uv), _ptr(k), _ptr(v), n, H, D, R,
                                                 _stream(stream)))
     return k, v
@@ -499,9 +516,9 @@ def mla_prefill_expanded(q, k, v, scale=SCALE, out=None, lse=None, status=None, 
     _require(lse, "lse", "f32", (B, L, H), optional=True)
     _require(status, "status", "i32", min_numel=1, optional=True)
     _check_cuda(q, k, v, out, lse, status)
-    out = torch.empty(B, L, H, D, dtype=torch.bfloat16, device=q.device) if out is None else out
+    out = _new(stream, (B, L, H, D), torch.bfloat16, q.device) if out is None else out
     if lse is None and want_lse:
-        lse = torch.empty(B, L, H, dtype=torch.float32, device=q.device)
+        lse = _new(stream, (B, L, H), torch.float32, q.device)
     _check("mla_prefill_expanded", lib().mla_prefill_expanded(
         _ptr(q), _ptr(k), _ptr(v), B, L, H, D, scale, _ptr(out), _ptr(lse), _ptr(status), _stream(stream)))
     return out, lse
@@ -517,7 +534,7 @@ def mla_debug_gather(mode, src, req, page_table=None, indices=None, B=None, Q=1,
     _require(status, "status", "i32", min_numel=1, optional=True)
     _check_cuda(src, req, page_table, indices, status)
     n = req.shape[0]
-    out = torch.empty(n, R, dtype=torch.bfloat16, device=src.device)
+    out = _new(stream, (n, R), torch.bfloat16, src.device)
     max_pages = page_table.shape[1] if page_table is not None else 0
     num_pages = src.shape[0] if mode == MODE_PAGED else 0
     K = indices.shape[2] if indices is not None else 0
@@ -772,7 +789,7 @@ def mla_kpool_keys(cache, pool, seq_lens=None, pooled=None, stream=None):
     _require(pooled, "pooled", "f32", (B, Lmax // pool, R), optional=True)
     _check_cuda(cache, seq_lens, pooled)
     if pooled is None:
-        pooled = torch.zeros(B, Lmax // pool, R, dtype=torch.float32, device=cache.device)
+        pooled = _new(stream, (B, Lmax // pool, R), torch.float32, cache.device, torch.zeros)
     _check("mla_kpool_keys", lib().mla_kpool_keys(_ptr(cache), _ptr(seq_lens), B, R, Lmax, pool, _ptr(pooled),
                                                   _stream(stream)))
     return pooled
@@ -792,7 +809,7 @@ def mla_kpool_select(pooled, w_query, pool, topk, seq_lens=None, with_tail=True,
         raise ValueError(f"pooled holds {pooled.shape[1]} pools per sequence, Lmax {Lmax} needs {Lmax // pool}")
     _check_cuda(pooled, w_query, seq_lens)
     W = topk + (pool - 1 if with_tail else 0)
-    out = torch.empty(B, Q, W, dtype=torch.int32, device=w_query.device)
+    out = _new(stream, (B, Q, W), torch.int32, w_query.device)
     _check("mla_kpool_select", lib().mla_kpool_select(
         _ptr(pooled), _ptr(w_query), _ptr(seq_lens), B, Q, R, Lmax, pool, topk, 1 if with_tail else 0, _ptr(out), W,
         _stream(stream)))

@@ -203,3 +203,44 @@ def test_outputs_of_a_call_on_another_stream_are_not_memory_that_is_still_writte
     got_rows = m.mla_cache_unpack(c.pool, c.table, start, 130, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got_rows, rows)
+
+
+@pytest.mark.parametrize("late", ["current", "side"])
+@pytest.mark.parametrize("form", ["packed", "window", "window_paged", "dense", "paged", "fused"])
+def test_decode_on_another_stream(form, late):
+    """mla_decode's own tensors are the stream's.  The current stream still writes freed tensors of
+    their sizes when the call is made (late = current), or the call's stream is behind and the current one
+    fills new tensors of their sizes meanwhile (late = side)."""
+    B = 2
+    c = Cache(B, 4, 12)
+    c.append(_rows((B, 130), 74))
+    w = [to_dev(synth.normal_bf16((64, 256, 512), 75, s, 512 ** -0.5)) for s in (synth.STREAM_WUK, synth.STREAM_WUV)]
+    q = to_dev(synth.normal_bf16((B, 1, 64, 256), 76, synth.STREAM_Q))
+    cache, pool = to_dev(_rows((B, 130), 77)), to_dev(_rows((12, PAGE), 78))
+    args, kw = {"packed": ((c.pool, c.lens), dict(mode=m.MODE_PACKED, page_table=c.table, window=64)),
+                "window": ((cache, c.lens), dict(window=64, sinks=2)),
+                "window_paged": ((pool, c.lens), dict(mode=m.MODE_PAGED, page_table=c.table, window=64)),
+                "dense": ((cache, c.lens), {}),
+                "paged": ((pool, c.lens), dict(mode=m.MODE_PAGED, page_table=c.table)),
+                "fused": ((cache, c.lens), dict(fused=True))}[form]
+    want = m.mla_decode(q, *w, *args, **kw, status=c.status)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    gate = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")  # some milliseconds of fills
+    own = [torch.empty(B, 1, 64, n, dtype=torch.bfloat16, device="cuda") for n in (512, 512, 256)]
+    own += [torch.empty_like(want[1]), torch.empty_like(m.new_workspace(B, 1))]
+    shapes = [(x.shape, x.dtype) for x in own]
+    with torch.cuda.stream(torch.cuda.current_stream() if late == "current" else s):
+        for _ in range(60):
+            gate.zero_()
+    if late == "current":
+        for x in own:
+            x.fill_(255)
+        del x
+    own = None
+    got = m.mla_decode(q, *w, *args, **kw, status=c.status, stream=s)
+    if late == "side":
+        own = [torch.full(shape, 255, dtype=dtype, device="cuda") for shape, dtype in shapes]
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
