@@ -133,6 +133,10 @@ __device__ void write_partial_table(const P &p, int lane) {
 // values 4t .. 4t + 3 of a partial, in the order that the attend kernel found convenient; the row
 // goes through shared memory to its latents' places, Order::latent.
 //
+// Only an empty partial (m = -inf, O never written) is left out.  One whose weight is zero in fp32
+// still counts: a NaN or an Inf in its sums reaches the result, as 0 x NaN does in the formula.
+constexpr float kEmpty = -1.f;  // in place of the weight of an empty partial
+
 // The places of sequence b's partials, from write_partial_table.
 struct Partials {
   int count, first, ts, T;
@@ -226,7 +230,7 @@ __global__ void __launch_bounds__(128, 8) combine_few_kernel(const P p, float un
       acc[hh].w *= a;
 #pragma unroll
       for (int j = 0; j < kChunk; ++j) {
-        if (mk[hh][j] == -INFINITY) continue;  // an empty partial's O was never written
+        if (mk[hh][j] == -INFINITY) continue;  // empty
         const float w = exp2f(mk[hh][j] - mx);
         den[hh] += w * lk[hh][j];
         acc[hh].x += w * ok[hh][j].x;
@@ -274,9 +278,9 @@ __global__ void __launch_bounds__(128 * kSlices) combine_many_kernel(const P p, 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     for (int k = lane; k < pt.count; k += 32) {
-      const float w = weight[k] == -INFINITY ? 0.f : exp2f(weight[k] - M);  // an empty partial's O was never written
+      const float w = weight[k] == -INFINITY ? kEmpty : exp2f(weight[k] - M);
       weight[k] = w;
-      if (w != 0.f) den += w * p.part_l[slots[k] * kHeads + h];
+      if (w != kEmpty) den += w * p.part_l[slots[k] * kHeads + h];
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
@@ -291,7 +295,7 @@ __global__ void __launch_bounds__(128 * kSlices) combine_many_kernel(const P p, 
   for (int k = slice; k < pt.count; k += kSlices) {
     const float w = weight[k];
     const float *at = p.part_o + (slots[k] * kHeads + h) * kLatent + 4 * t;
-    const float4 o = w != 0.f ? *reinterpret_cast<const float4 *>(at) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 o = w != kEmpty ? *reinterpret_cast<const float4 *>(at) : make_float4(0.f, 0.f, 0.f, 0.f);
     acc.x += w * o.x;
     acc.y += w * o.y;
     acc.z += w * o.z;
@@ -360,9 +364,9 @@ __global__ void __launch_bounds__(kRowThreads) combine_row_kernel(const P p, flo
 #pragma unroll
     for (int j = 0; j < kMaxPartials / 32; ++j) {
       const int k = lane + 32 * j;
-      const float w = m[j] == -INFINITY ? 0.f : exp2f(m[j] - M);  // an empty partial's O was never written
+      const float w = m[j] == -INFINITY ? kEmpty : exp2f(m[j] - M);
       if (k < pt.count) weight[k] = w;
-      den += w * l[j];
+      if (w != kEmpty) den += w * l[j];
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
@@ -374,7 +378,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_row_kernel(const P p, flo
   __syncthreads();
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](float w, const float4 &o) {
-    if (w == 0.f) return;
+    if (w == kEmpty) return;
     acc.x += w * o.x;
     acc.y += w * o.y;
     acc.z += w * o.z;

@@ -296,3 +296,36 @@ def test_merges_read_only_what_the_call_wrote(q_len, lens, window, sinks):
     assert int(st.item()) == 0
     assert torch.equal(o, again) and torch.equal(lse, lse_again)
     _check(lens, values, qt, window, sinks, o, lse)
+
+
+# Every form of the merge, a tile per CTA: a single row; few sequences; more; as many as CTA groups.
+TILE_EACH = [[12801], [6401, 6400], [257] * 20, [257] * 40 + [0] * 110]
+
+
+@pytest.mark.parametrize("what", ["query", "row", "last row"])
+@pytest.mark.parametrize("lens", TILE_EACH, ids=[f"{len(x)}x{max(x)}" for x in TILE_EACH])
+def test_nan_shows_whatever_its_weight(lens, what):
+    """Head 0 of every sequence scores 200 and more at row 3 and about 0 elsewhere: the other tiles'
+    partials have the weight 2^-288 or less, zero in fp32, and a NaN in them still counts (0 x NaN)."""
+    lens, table, pool, _ = _setup(lens, 0, seed=40)
+    qt = synthetic_qtilde(len(lens), 1, seed=41)
+    q = oracle.widen(qt)[:, 0, 0]
+    assert np.abs(q).sum(axis=1).min() > 200
+    pool[..., 256:] = 0x01  # scales of 2^-9
+    high = oracle.packed_quantise(np.sign(q) * 16.0)
+    for b in np.flatnonzero(lens):
+        pool[table[b, 0], 3] = high[b]
+    if what == "query":
+        qt[0, 0, 5, 100] = 0x7FC0
+    else:
+        j = int(lens[0]) - 1 if what == "last row" else 200
+        pool[table[0, j // PAGE], j % PAGE, 256 + 7] = 0x7F
+    st = _status()
+    o, lse = m.mla_attend_packed(to_dev(qt), torch.from_numpy(pool).cuda(), ints_to_dev(table), ints_to_dev(lens), status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    bad = [5] if what == "query" else list(range(64))
+    fine = [h for h in range(64) if h not in bad]
+    assert torch.isnan(o[0, 0, bad]).all() and torch.isnan(lse[0, 0, bad]).all()
+    assert torch.isfinite(o[0, 0, fine].float()).all() and torch.isfinite(lse[0, 0, fine]).all()
+    assert torch.isfinite(o[1:].float()).all() and torch.isfinite(lse[1:][ints_to_dev(lens[1:]) > 0]).all()

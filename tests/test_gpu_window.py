@@ -186,3 +186,51 @@ def test_merges_read_only_what_the_call_wrote(q_len, lens, window, sinks):
     assert int(st.item()) == 0
     assert torch.equal(o, again) and torch.equal(lse, lse_again)
     _check(lens, oracle.widen(bits), qt, window, sinks, o, lse)
+
+
+# Every form of the merge, a tile per CTA: a single row; few sequences; more; as many as CTA groups.
+TILE_EACH = [[6401], [3201, 3200], [129] * 20, [129] * 40 + [0] * 110]
+
+
+def _aligned(lens, seed):
+    """Head 0 of every sequence scores 200 and more at row 3 and about 0 elsewhere: every partial but the
+    first tile's has the weight 2^-288 or less, zero in fp32."""
+    bits = synth.normal_bf16((len(lens), max(lens), R), seed, synth.STREAM_CACHE, 0.01)
+    qt = synthetic_qtilde(len(lens), 1, seed=seed + 1)
+    q = oracle.widen(qt)[:, 0, 0]
+    assert (q != 0).all() and np.abs(q).sum(axis=1).min() > 200
+    bits[:, 3] = synth.f64_to_bf16_bits(np.sign(q) * 16.0)
+    return bits, qt, q
+
+
+def _finite_but_first(lens, o, lse):
+    assert torch.isfinite(o[1:].float()).all() and not torch.isnan(lse[1:]).any()
+    assert torch.isfinite(lse[1:][ints_to_dev(lens)[1:] > 0]).all()
+
+
+@pytest.mark.parametrize("alone", [False])
+@pytest.mark.parametrize("lens", TILE_EACH)
+def test_a_nan_survives_a_weight_of_zero(lens, alone):
+    """In a row (alone: the only one of its tile) that counts for nothing beside another tile's: 0 x NaN."""
+    bits, qt, _ = _aligned(lens, 44)
+    bits[0, lens[0] - 1 if alone else 100, 200] = NAN
+    st = _status()
+    o, lse = m.mla_attend_window_dense(to_dev(qt), to_dev(bits), 100000, 0, ints_to_dev(lens), status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert torch.isnan(o[0]).all() and torch.isnan(lse[0]).all()
+    _finite_but_first(lens, o, lse)
+
+
+@pytest.mark.parametrize("alone", [False])
+@pytest.mark.parametrize("lens", TILE_EACH)
+def test_an_infinite_row_of_weight_zero_gives_nan(lens, alone):
+    """Its score is -Inf for head 0: weight 0, and 0 x Inf in every latent; lse is that of the other rows."""
+    bits, qt, q = _aligned(lens, 46)
+    bits[0, lens[0] - 1 if alone else 100] = np.where(q[0] > 0, 0xFF80, 0x7F80)
+    st = _status()
+    o, lse = m.mla_attend_window_dense(to_dev(qt), to_dev(bits), 100000, 0, ints_to_dev(lens), status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert torch.isnan(o[0, 0, 0]).all() and torch.isfinite(lse[0, 0, 0])
+    _finite_but_first(lens, o, lse)
