@@ -137,9 +137,10 @@ mla_status mla_attend_indexed(const uint16_t *q_tilde, const uint16_t *cache, co
  * rows j <= t with t - j < window (its own row and the window - 1 before it) or j < sinks (the first
  * rows of the sequence, which stay visible).  window >= 1, sinks >= 0; everything else as there.
  * Only tiles with a visible row are read: paged, a page outside every query's window and the sinks
- * need not be mapped.  Rows that a query does not see may hold any bits.  lse sums the unrounded
- * weights (mla_attend_dense sums them as rounded to bf16), so the two agree to rounding where the
- * window covers the sequence.  Lmax, max_pages * 64 < 2^31 - 64.  The pages describe no window.
+ * need not be mapped.  Rows that a query does not see may hold any bits.  A NaN in a row that it sees
+ * gives NaN, one in a head of q~ in that head.  lse sums the unrounded weights (mla_attend_dense sums
+ * them as rounded to bf16), so the two agree to rounding where the window covers the sequence.
+ * Lmax, max_pages * 64 < 2^31 - 64.  The pages describe no window.
  */
 mla_status mla_attend_window_dense(const uint16_t *q_tilde, const uint16_t *cache, const int32_t *seq_lens, int B, int Q,
                                    int H, int R, int Lmax, float scale, int window, int sinks, void *workspace,

@@ -19,6 +19,7 @@
 // measured copy peak for distinct rows); around that, for windows of some thousand rows, 20 us of
 // start-up, partial stores and combine.  Measured with the merge: 32 x (4,096 + 64) of 8,192 rows
 // 41.7 us; 16 x 6 queries, window 4,095 + 5, 89-91 us.
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -500,7 +501,9 @@ __device__ void softmax_role(const WindowParams &p, const Shared &sh, uint32_t t
     const long long slot = split::partial_slot(p, kModePaged, g, sg.s, iq);
     if (tid < 32) {
       const int c = col0 + tid;
-      p.part_m[slot * kRows + c] = m_used[c];
+      // -inf marks an empty partial; this one counts even where every score is NaN (which the
+      // running max passes over) or -Inf
+      p.part_m[slot * kRows + c] = fmaxf(m_used[c], -FLT_MAX);
       p.part_l[slot * kRows + c] = red[c] + red[kRows + c] + red[2 * kRows + c] + red[3 * kRows + c];
     }
     float *po = p.part_o + slot * kRows * kLatent;

@@ -208,7 +208,40 @@ def _finite_but_first(lens, o, lse):
     assert torch.isfinite(lse[1:][ints_to_dev(lens)[1:] > 0]).all()
 
 
-@pytest.mark.parametrize("alone", [False])
+@pytest.mark.parametrize("lens", TILE_EACH)
+def test_a_nan_query_gives_nan(lens):
+    """The whole head, and no other."""
+    bits = synth.normal_bf16((len(lens), max(lens), R), 40, synth.STREAM_CACHE)
+    qt = synthetic_qtilde(len(lens), 1, seed=41)
+    bad = qt.copy()
+    bad[0, 0, 5, 100] = NAN
+    args = (to_dev(bits), 1000, 3, ints_to_dev(lens))
+    st = _status()
+    want, lse_want = m.mla_attend_window_dense(to_dev(qt), *args, status=st)
+    o, lse = m.mla_attend_window_dense(to_dev(bad), *args, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert torch.isnan(o[0, 0, 5]).all() and torch.isnan(lse[0, 0, 5])
+    o[0, 0, 5], lse[0, 0, 5] = want[0, 0, 5], lse_want[0, 0, 5]
+    _check(lens[:2], oracle.widen(bits[:2]), qt[:2], 1000, 3, o[:2], lse[:2])
+
+
+@pytest.mark.parametrize("window", [1, 64, 100000])
+@pytest.mark.parametrize("lens", TILE_EACH)
+def test_a_nan_in_a_seen_row_gives_nan(lens, window):
+    """The only seen row of its tile and CTA."""
+    bits = synth.normal_bf16((len(lens), max(lens), R), 42, synth.STREAM_CACHE)
+    bits[0, lens[0] - 1, 77] = NAN
+    qt = synthetic_qtilde(len(lens), 1, seed=43)
+    st = _status()
+    o, lse = m.mla_attend_window_dense(to_dev(qt), to_dev(bits), window, 0, ints_to_dev(lens), status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert torch.isnan(o[0]).all() and torch.isnan(lse[0]).all()
+    _finite_but_first(lens, o, lse)
+
+
+@pytest.mark.parametrize("alone", [False, True])
 @pytest.mark.parametrize("lens", TILE_EACH)
 def test_a_nan_survives_a_weight_of_zero(lens, alone):
     """In a row (alone: the only one of its tile) that counts for nothing beside another tile's: 0 x NaN."""
@@ -222,7 +255,7 @@ def test_a_nan_survives_a_weight_of_zero(lens, alone):
     _finite_but_first(lens, o, lse)
 
 
-@pytest.mark.parametrize("alone", [False])
+@pytest.mark.parametrize("alone", [False, True])
 @pytest.mark.parametrize("lens", TILE_EACH)
 def test_an_infinite_row_of_weight_zero_gives_nan(lens, alone):
     """Its score is -Inf for head 0: weight 0, and 0 x Inf in every latent; lse is that of the other rows."""
