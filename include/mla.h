@@ -324,7 +324,8 @@ mla_status mla_attend_packed(const uint16_t *q_tilde, const uint8_t *pool, const
  *   other entries map too (refs > 1 at the call) by a copy of its own.
  * mla_pages_fork: sequence children[k] becomes a copy of sequence parents[k]: full pages are shared,
  *   the partial last page is copied to a fresh one, the length is set.  A child must be empty (all
- *   entries -1), occur once in children and not in parents.  Rows that were there before a fork
+ *   entries -1), occur once in children and not in parents.  A full page of the parent may be unmapped
+ *   and is the child's then too; the partial last one must be mapped.  Rows that were there before a fork
  *   are shared: make room by mla_pages_reserve before rewriting any of them (an append after a
  *   fork needs no more than usual; mla_cache_truncate_* beyond the fork point would write them).
  * mla_pages_release: unmaps the entries at and behind ceil(L_b / 64): after a truncation, or, with
@@ -333,6 +334,8 @@ mla_status mla_attend_packed(const uint16_t *q_tilde, const uint8_t *pool, const
  *   number, to the free pages below it, in order; refs and all B tables follow.  n_used: device int32.
  *   Afterwards pages n_used .. num_pages - 1 are free.  An entry that maps a free page stays as it is
  *   and sets MLA_ERR_INDEX.
+ * A caller that attends within windows only may give pages back that none reaches any more: it sets
+ *   their entries to -1 and takes one off refs for each.
  * A sequence or list entry whose positions, pages or indexes are out of range (or, fork: as above) is
  * left untouched and sets MLA_ERR_INDEX; one whose pages are no longer free, and every later one
  * that needs a page, is left untouched and sets MLA_ERR_PAGES; the others proceed.  Pages keep

@@ -107,7 +107,8 @@ __device__ int reserve_demand(const Book &bk, int b, int Q) {
 }
 
 // Fork k is sound: both sequences exist, the child is empty and stands nowhere else in the list,
-// the parent's pages are mapped.  Its demand: the page of the parent's partial last page.
+// the parent's full pages are mapped or unmapped (given back behind a window), its partial last page is
+// mapped.  Its demand: the copy of that one.
 __device__ int fork_demand(const Book &bk, const int32_t *parents, const int32_t *children, int n, int k) {
   const int par = parents[k], child = children[k];
   bool ok = par >= 0 && par < bk.B && child >= 0 && child < bk.B && par != child;
@@ -119,7 +120,10 @@ __device__ int fork_demand(const Book &bk, const int32_t *parents, const int32_t
     partial = L % kPageTokens != 0;
     for (int e = threadIdx.x; e < bk.max_pages; e += kThreads) {
       ok = ok && bk.table[(long long)child * bk.max_pages + e] == -1;
-      if ((long long)e * kPageTokens < L) ok = ok && mapped(bk, bk.table[(long long)par * bk.max_pages + e]);
+      if ((long long)e * kPageTokens >= L) continue;
+      const int page = bk.table[(long long)par * bk.max_pages + e];
+      const bool full = (e + 1LL) * kPageTokens <= L;
+      ok = ok && (mapped(bk, page) || (full && page == -1));
     }
   }
   return __syncthreads_and(ok) ? partial : kBad;
@@ -316,6 +320,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const Book bk, const int
   __shared__ int fresh;
   for (int e = threadIdx.x; e < full; e += kThreads) {
     const int page = from[e];
+    if (page == -1) continue;  // as the child's entry
     to[e] = page;
     atomicAdd(&bk.refs[page], 1);
   }

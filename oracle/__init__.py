@@ -484,7 +484,8 @@ class PageBook:
             ok = ok and bool((before[child] == -1).all()) and 0 <= lens0[par] <= max_pages * self.page
             if ok:
                 used = before[par, : -(-int(lens0[par]) // self.page)]
-                ok = bool(((used >= 0) & (used < len(self.refs))).all())
+                ok = bool(((used >= -1) & (used < len(self.refs))).all())
+                ok = ok and (int(lens0[par]) % self.page == 0 or used[-1] >= 0)  # full pages may be unmapped
             if not ok:
                 entries.append(None)
                 continue
@@ -496,7 +497,8 @@ class PageBook:
                 full = int(lens0[par]) // self.page
                 self.table[child, :full] = before[par, :full]
                 for p in before[par, :full]:
-                    self.refs[p] += 1
+                    if p >= 0:
+                        self.refs[p] += 1
                 self.lens[child] = lens0[par]
         return status
 

@@ -245,3 +245,65 @@ def test_compaction_flags_entries_that_map_free_pages(low):
     # used pages at or above 8 move, in order, to the free ones: low {8, 9} to {1, 2}, else {8} to {2}
     assert table[1, 2].item() == (1 if low else 2) and table[2, 0].item() == (2 if low else 1)
     assert int(pool[int(table[1, 2].item()), 0, 0].item()) == 8
+
+
+def _give_back(s, b, entries):
+    """What a caller does with pages that no window reaches any more."""
+    for k in entries:
+        s.book.refs[s.book.table[b, k]] -= 1
+        s.book.table[b, k] = -1
+    s.table.copy_(ints_to_dev(s.book.table))
+    s.refs.copy_(ints_to_dev(s.book.refs))
+
+
+def test_a_sequence_whose_early_pages_were_given_back():
+    """Its fork leaves the same entries unmapped; both go on, move, and give their tails back."""
+    rng = np.random.default_rng(7)
+    s = _state(rng, 4, [450, 320, 0, 0], 9, 40)
+    _give_back(s, 0, [1, 2, 4])
+    _give_back(s, 1, [0, 1, 2, 3])
+    assert s.call("fork", [0, 1], [2, 3]) == "ok"  # a partial last page, and none
+    assert s.book.lens.tolist() == [450, 320, 450, 320]
+    assert (s.book.table[2, :9] < 0).tolist() == [False, True, True, False, True, False, False, False, True]
+    assert (s.book.table[3, :5] < 0).tolist() == [True] * 4 + [False]
+    assert s.call("reserve", 70) == "ok"
+    assert s.call("compact") == "ok"
+    for b in range(4):
+        s.book.lens[b] -= 70
+        s.lens[b] -= 70
+    assert s.call("release") == "ok"
+    assert s.call("reserve", 6) == "ok"            # into pages that parent and child share
+
+
+def test_a_fork_needs_the_page_it_copies():
+    rng = np.random.default_rng(8)
+    s = _state(rng, 3, [450, 0, 0], 9, 40)
+    _give_back(s, 0, [7])                          # the partial last page
+    assert s.call("fork", [0], [1]) == "index"
+    s = _state(rng, 3, [450, 0, 0], 9, 40)
+    for bad in (-2, 40, 1 << 30):
+        s.book.table[0, 2] = bad
+        s.book.refs[:] = np.bincount(s.book.table[(s.book.table >= 0) & (s.book.table < 40)], minlength=40)
+        s.table.copy_(ints_to_dev(s.book.table))
+        s.refs.copy_(ints_to_dev(s.book.refs))
+        assert s.call("fork", [0], [1]) == "index"
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_windowed_attention_of_a_fork_without_early_pages(packed):
+    """Parent and child attend the same rows; the window's pages and the sink's are all that is mapped."""
+    rng = np.random.default_rng(9)
+    s = _state(rng, 2, [450, 0], 9, 40)
+    _give_back(s, 0, [1, 2, 3, 4])                 # window 100 + sinks 4: pages 0, 5, 6, 7
+    if packed:
+        pool = torch.randint(0, 256, (40, PAGE, 288), dtype=torch.uint8, device="cuda")
+        pool[..., 256:] = 0x38                     # scales of 1
+    else:
+        pool = torch.randn(40, PAGE, 512, device="cuda").to(torch.bfloat16)
+    m.mla_pages_fork(pool, s.table, s.lens, s.refs, ints_to_dev([0]), ints_to_dev([1]), status=s.status)
+    qt = torch.randn(1, 1, 64, 512, device="cuda").to(torch.bfloat16).repeat(2, 1, 1, 1)
+    attend = m.mla_attend_packed if packed else m.mla_attend_window_paged
+    o, lse = attend(qt, pool, s.table, s.lens, window=100, sinks=4, status=s.status)
+    torch.cuda.synchronize()
+    assert int(s.status.item()) == 0
+    assert torch.equal(o[0], o[1]) and torch.equal(lse[0], lse[1]) and torch.isfinite(o.float()).all()
