@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import operator
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -172,9 +173,13 @@ def _check_current(*tensors):
 
 
 def _require_int32(**values):
-    """ctypes would wrap a larger number without a word."""
+    """ctypes would wrap a larger number, of any integer type, without a word."""
     for name, v in values.items():
-        if isinstance(v, int) and not -2**31 <= v < 2**31:
+        try:
+            v = operator.index(v)
+        except TypeError:
+            continue  # not an integer: ctypes refuses it
+        if not -2**31 <= v < 2**31:
             raise ValueError(f"{name} must fit 32 bits, got {v}")
 
 

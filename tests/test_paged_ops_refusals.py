@@ -3,6 +3,7 @@ device (C ABI), and tensors whose dtype, layout or size would let a kernel addre
 them (binding).  None of these calls launches anything."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
@@ -201,3 +202,16 @@ def test_numbers_past_32_bits(lib, big):
                        ("n", lambda: m.mla_pages_workspace_bytes(big, 1))):
         with pytest.raises(ValueError, match=f"^{name} must fit 32 bits"):
             call()
+
+
+@pytest.mark.parametrize("big", [2**31, 2**32 + 1, -2**31 - 1])
+def test_numpy_and_tensor_numbers_past_32_bits(lib, big):
+    """They have no Python int's type, and ctypes wraps them all the same."""
+    for make in (np.int64, torch.tensor):
+        for name, call in (("window", lambda: m.mla_attend_window_dense(None, None, make(big))),
+                           ("sinks", lambda: m.mla_attend_packed(None, None, None, None, sinks=make(big))),
+                           ("q_len", lambda: m.mla_pages_reserve(None, None, None, None, make(big))),
+                           ("n", lambda: m.mla_pages_workspace_bytes(make(big), 1))):
+            with pytest.raises(ValueError, match=f"^{name} must fit 32 bits"):
+                call()
+    assert m.mla_pages_workspace_bytes(np.int64(3), np.int32(5)) == m.mla_pages_workspace_bytes(3, 5)
