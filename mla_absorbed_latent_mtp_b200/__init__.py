@@ -833,6 +833,8 @@ def mla_decode(q, w_uk, w_uv, cache, seq_lens=None, *, mode=MODE_DENSE, page_tab
         raise ValueError("fused=True has no windowed or packed form")
     if window and mode == MODE_INDEXED:
         raise ValueError("index lists take no window")
+    if window or mode == MODE_PACKED:  # as their attention refuses it, before anything is launched
+        _check_current(q, w_uk, w_uv, cache, seq_lens, page_table, workspace, status)
     qt = mla_absorb_q(q, w_uk, stream=stream)
     if fused:
         if mode == MODE_DENSE:

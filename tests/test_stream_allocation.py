@@ -107,3 +107,23 @@ def test_a_stream_of_another_device_is_refused(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     with pytest.raises(ValueError, match="the stream is on cuda:1, the current device is cuda:0"):
         m._allocating_on(Stream())
+
+
+@pytest.mark.parametrize("name", ["decode_window", "decode_window_paged", "decode_packed"])
+def test_decode_launches_nothing_for_another_device(monkeypatch, name):
+    """The attention refuses tensors that are not on the current device; q~ is not computed before."""
+    launched = []
+
+    class Lib:
+        def __getattr__(self, f):
+            return lambda *args: launched.append(f) or 0
+
+    check_current = m._check_current
+    Record(monkeypatch)
+    monkeypatch.setattr(m, "_lib", Lib())
+    monkeypatch.setattr(m, "_check_current", check_current)
+    monkeypatch.setattr(m, "_check_cuda", lambda *t: 1)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="tensors are on cuda:1, the current device is cuda:0"):
+        CALLS[name]()
+    assert not launched
