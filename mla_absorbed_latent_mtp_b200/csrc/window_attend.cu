@@ -528,9 +528,10 @@ __device__ void softmax_role(const WindowParams &p, const Shared &sh, uint32_t t
 
 // ------------------------------------------------------------------ kernel
 template <bool kPaged>
-// Bounds for 384 threads: eleven warps put three on some SM sub-partitions, whose 16K
-// registers then cap a thread at 168 (the 352-thread bound alone would allow 184).
-__global__ void __launch_bounds__(kThreads, 1)
+// Bounds for 384 threads: eleven warps put three on some SM sub-partitions, whose 16K registers then
+// cap a thread at 168, and the bound of 352 threads would let the compiler give it 184, with which no
+// launch would succeed.  Both forms use 156 with either bound.
+__global__ void __launch_bounds__(384, 1)
     attend_window_kernel(const __grid_constant__ CUtensorMap tm_cache, const __grid_constant__ CUtensorMap tm_qt,
                          const WindowParams p) {
   extern __shared__ uint8_t smem_raw[];
