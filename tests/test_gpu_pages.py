@@ -307,3 +307,34 @@ def test_windowed_attention_of_a_fork_without_early_pages(packed):
     torch.cuda.synchronize()
     assert int(s.status.item()) == 0
     assert torch.equal(o[0], o[1]) and torch.equal(lse[0], lse[1]) and torch.isfinite(o.float()).all()
+
+
+def test_two_page_operations_at_once():
+    """On two streams, each with its own state and workspace."""
+    def start(k):
+        return _state(np.random.default_rng(20 + k), 40, [50 + 7 * b for b in range(30)] + [0] * 10, 12, 400, 256)
+
+    def step(s, ws, n_used):
+        m.mla_pages_fork(s.pool, s.table, s.lens, s.refs, kids[0], kids[1], workspace=ws, status=s.status)
+        m.mla_pages_reserve(s.pool, s.table, s.lens, s.refs, 66, workspace=ws, status=s.status)
+        m.mla_pages_release(s.table, s.lens, s.refs, status=s.status)
+        m.mla_pages_compact(s.pool, s.table, s.refs, n_used=n_used, workspace=ws, status=s.status)
+
+    kids = ints_to_dev(list(range(10))), ints_to_dev(list(range(30, 40)))
+    n_useds = [ints_to_dev([0]) for _ in range(2)]
+    both = [start(k) for k in range(2)]
+    wss = [m.new_pages_workspace(40, 400) for _ in both]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in both]
+    for s, ws, n_used, st in zip(both, wss, n_useds, streams):
+        with torch.cuda.stream(st):
+            step(s, ws, n_used)
+    torch.cuda.synchronize()
+    for k, s in enumerate(both):
+        assert int(s.status.item()) == 0
+        s.book.fork(list(range(10)), list(range(30, 40)))
+        s.book.reserve(66)
+        s.book.release()
+        assert int(n_useds[k].item()) == s.book.compact()
+        for got, want in ((s.table, s.book.table), (s.lens, s.book.lens), (s.refs, s.book.refs), (s.pool, s.book.pool)):
+            assert np.array_equal(got.cpu().numpy(), want)

@@ -267,3 +267,66 @@ def test_an_infinite_row_of_weight_zero_gives_nan(lens, alone):
     assert int(st.item()) == 0
     assert torch.isnan(o[0, 0, 0]).all() and torch.isfinite(lse[0, 0, 0])
     _finite_but_first(lens, o, lse)
+
+
+@pytest.mark.parametrize("window,sinks", [(1000, 0), (2**31 - 1, 2**31 - 1)])
+def test_a_window_over_everything_matches_float64(window, sinks):
+    lens = np.array([1000, 333, 64], dtype=np.int32)
+    bits = synth.normal_bf16((3, 1000, R), 8, synth.STREAM_CACHE)
+    qt = synthetic_qtilde(3, 2, seed=9)
+    st = _status()
+    o, lse = m.mla_attend_window_dense(to_dev(qt), to_dev(bits), window, sinks, ints_to_dev(lens), status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    _check(lens, oracle.widen(bits), qt, 0, 0, o, lse)
+
+
+def _step_inputs(seed, n):
+    lens = np.array([900 + 50 * n, 64, 5, 333], dtype=np.int32)
+    table, P = synth.page_layout(lens, seed)
+    pool = to_dev(synth.normal_bf16((P, PAGE, R), seed, synth.STREAM_CACHE))
+    return to_dev(synthetic_qtilde(4, 2, seed=seed + 1)), pool, ints_to_dev(table), ints_to_dev(lens)
+
+
+def test_captured_and_replayed():
+    """Dense and paged calls in one graph, with short and empty lists, replayed on other lengths and queries."""
+    qt, pool, table, lens = _step_inputs(50, 0)
+    cache = to_dev(synth.normal_bf16((4, 950, R), 52, synth.STREAM_CACHE))
+    ws, st = m.new_workspace(4, 2), _status()
+
+    def step():
+        return (*m.mla_attend_window_paged(qt, pool, table, lens, 100, 3, workspace=ws, status=st),
+                *m.mla_attend_window_dense(qt, cache, 300, 0, lens, workspace=ws, status=st))
+
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        out = step()
+    for k, now in enumerate(([900, 64, 5, 333], [900, 0, 0, 1], [0, 0, 0, 0], [2, 64, 5, 200])):
+        lens.copy_(ints_to_dev(now))
+        qt.copy_(to_dev(synthetic_qtilde(4, 2, seed=53 + k)))
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in out]
+        for x, y in zip(got, step()):
+            assert torch.equal(x, y)
+    assert int(st.item()) == 0
+
+
+def test_two_streams_at_once():
+    """Each with its own workspace, and lists so short that most CTAs have nothing to load."""
+    inputs = [_step_inputs(60, 0), _step_inputs(62, 1)]
+    wss = [m.new_workspace(4, 2) for _ in inputs]
+    sts = [_status() for _ in inputs]
+    alone = [m.mla_attend_window_paged(*x, 100, 3, workspace=ws) for x, ws in zip(inputs, wss)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in inputs]
+    for _ in range(20):
+        got = []
+        for x, ws, st, s in zip(inputs, wss, sts, streams):
+            with torch.cuda.stream(s):
+                got.append(m.mla_attend_window_paged(*x, 100, 3, workspace=ws, status=st))
+        torch.cuda.synchronize()
+        for x, y, st in zip(got, alone, sts):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1]) and int(st.item()) == 0
