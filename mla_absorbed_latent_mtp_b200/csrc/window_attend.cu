@@ -47,6 +47,9 @@ constexpr int kThreads = 352;  // producer, score MMA, 8 softmax warps, value MM
 constexpr int kSoftmaxWarps = 8;
 constexpr float kTau = 8.0f;  // lazy rescale: the running max is raised only when a score
                               // exceeds it by more than 2^8 (probabilities stay <= 256)
+// The running max before any score.  Finite, since -inf marks an empty partial: one that has seen
+// only NaN scores, which the max passes over, or -Inf is not empty.
+constexpr float kLowest = -FLT_MAX;
 
 constexpr int kOffC = 0;
 constexpr int kOffQt = kOffC + kSlots * kSlotBytes;
@@ -354,7 +357,7 @@ __device__ void softmax_role(const WindowParams &p, const Shared &sh, uint32_t t
   float *m_used = sh.m_used;    // [64]
   float *alpha = sh.alpha;      // [64]
   uint32_t n = 0, o_use = 0;    // tiles seen by this CTA, segments finished
-  if (tid < 32) m_used[col0 + tid] = -INFINITY;
+  if (tid < 32) m_used[col0 + tid] = kLowest;
   named_bar_sync(bar_id, 128);
   SegIter<kPaged> it(range, iq);
   Seg sg;
@@ -372,7 +375,7 @@ __device__ void softmax_role(const WindowParams &p, const Shared &sh, uint32_t t
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       l_part[c] = 0.f;
-      m_reg[c] = -INFINITY;
+      m_reg[c] = kLowest;
     }
     for (int t = sg.lo; t < sg.hi; t = sg.next(t), ++n) {
       const uint32_t sb = n & 1;
@@ -422,7 +425,7 @@ __device__ void softmax_role(const WindowParams &p, const Shared &sh, uint32_t t
           const float mt = fmaxf(fmaxf(red[c], red[kRows + c]), fmaxf(red[2 * kRows + c], red[3 * kRows + c]));
           const float mo = m_used[c];
           const float mn = fmaxf(mo, mt);
-          alpha[c] = (mn == -INFINITY) ? 1.f : fast_exp2(mo - mn);
+          alpha[c] = fast_exp2(mo - mn);
           m_used[c] = mn;
         }
         named_bar_sync(bar_id, 128);
@@ -501,9 +504,7 @@ __device__ void softmax_role(const WindowParams &p, const Shared &sh, uint32_t t
     const long long slot = split::partial_slot(p, kModePaged, g, sg.s, iq);
     if (tid < 32) {
       const int c = col0 + tid;
-      // -inf marks an empty partial; this one counts even where every score is NaN (which the
-      // running max passes over) or -Inf
-      p.part_m[slot * kRows + c] = fmaxf(m_used[c], -FLT_MAX);
+      p.part_m[slot * kRows + c] = m_used[c];
       p.part_l[slot * kRows + c] = red[c] + red[kRows + c] + red[2 * kRows + c] + red[3 * kRows + c];
     }
     float *po = p.part_o + slot * kRows * kLatent;
@@ -521,7 +522,7 @@ __device__ void softmax_role(const WindowParams &p, const Shared &sh, uint32_t t
     if (lane == 0) mbar_arrive(&bar[kBarOEmpty]);
     ++o_use;
     named_bar_sync(bar_id, 128);
-    if (tid < 32) m_used[col0 + tid] = -INFINITY;
+    if (tid < 32) m_used[col0 + tid] = kLowest;
     named_bar_sync(bar_id, 128);
   }
 }
