@@ -12,7 +12,6 @@ for s.  Its arguments are the caller's to order before the call and to keep unti
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import operator
 import os
@@ -175,44 +174,31 @@ def _check_current(*tensors):
 def _require_int32(**values):
     """ctypes would wrap a larger number, of any integer type, without a word."""
     for name, v in values.items():
-        try:
-            v = operator.index(v)
-        except TypeError:
-            continue  # not an integer: ctypes refuses it
+        if type(v) is not int:
+            try:
+                v = operator.index(v)
+            except TypeError:
+                continue  # not an integer: ctypes refuses it
         if not -2**31 <= v < 2**31:
             raise ValueError(f"{name} must fit 32 bits, got {v}")
 
 
-def _allocating_on(stream):
-    """Memory made in this context is the `stream`'s of the call, which uses it first: made on the
+def _on(stream, call, *args):
+    """call(*args) on `stream`.  The whole call runs with it as the current stream, so that its memory
+    (results, workspace, intermediates) is the `stream`'s, which uses it first: made on the caller's
     current stream, it could be memory that kernels pending there still write, and, dropped when
-    the call returns, memory that the next tensor there is given while `stream` still reads it."""
-    if stream is None:
-        return contextlib.nullcontext()
+    the call returns, memory that the next tensor there is given while `stream` still reads it.
+    torch's allocator is told that the results are read on the caller's stream too."""
     cuda = _get_torch().cuda
     if stream.device_index != cuda.current_device():
         raise ValueError(f"the stream is on cuda:{stream.device_index}, the current device is cuda:{cuda.current_device()}")
-    return cuda.stream(stream)
-
-
-def _read_here(stream, *tensors):
-    """Tells torch's allocator that results made on `stream` are read on the current stream too."""
-    if stream is not None:
-        current = _get_torch().cuda.current_stream()
-        for t in tensors:
-            if t is not None:
-                t.record_stream(current)
-
-
-def _new(stream, shape, dtype, device, make=None):
-    """A result of a call on `stream`."""
-    make = make or _get_torch().empty
-    if stream is None:
-        return make(shape, dtype=dtype, device=device)
-    with _allocating_on(stream):
-        t = make(shape, dtype=dtype, device=device)
-    _read_here(stream, t)
-    return t
+    with cuda.stream(stream):
+        out = call(*args)
+    current = cuda.current_stream()
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(current)
+    return out
 
 
 def _require(t, name, dtype, shape=None, min_numel=None, optional=False):
@@ -251,16 +237,17 @@ def mla_attend_workspace_bytes(B: int, Q: int, heads: int = H, latent: int = R) 
     return int(lib().mla_attend_workspace_bytes(B, Q, heads, latent))
 
 
-def new_workspace(B: int, Q: int, stream=None):
-    """Allocate (with torch) the workspace the attend calls need, on `stream` if it is given."""
+def new_workspace(B: int, Q: int):
+    """Allocate (with torch) the workspace the attend calls need."""
     torch = _get_torch()
     n = mla_attend_workspace_bytes(B, Q)
-    with _allocating_on(stream):
-        return torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+    return torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
 
 
 def mla_absorb_q(q, w_uk, q_tilde=None, stream=None):
     """q [n, H, D] or [B, Q, H, D] bf16, w_uk [H, D, R] bf16 -> q_tilde [..., H, R] bf16."""
+    if stream is not None:
+        return _on(stream, mla_absorb_q, q, w_uk, q_tilde)
     torch = _get_torch()
     _require(q, "q", "bf16")
     if q.dim() < 3 or tuple(q.shape[-2:]) != (H, D):
@@ -270,13 +257,15 @@ def mla_absorb_q(q, w_uk, q_tilde=None, stream=None):
     _require(q_tilde, "q_tilde", "bf16", tuple(q.shape[:-1]) + (R,), optional=True)
     _check_cuda(q, w_uk, q_tilde)
     if q_tilde is None:
-        q_tilde = _new(stream, tuple(q.shape[:-1]) + (R,), torch.bfloat16, q.device)
+        q_tilde = torch.empty(*q.shape[:-1], R, dtype=torch.bfloat16, device=q.device)
     _check("mla_absorb_q", lib().mla_absorb_q(_ptr(q), _ptr(w_uk), _ptr(q_tilde), n, H, D, R, _stream(stream)))
     return q_tilde
 
 
 def mla_up_proj(o_latent, w_uv, out=None, stream=None):
     """o_latent [..., H, R] bf16, w_uv [H, D, R] bf16 -> out [..., H, D] bf16."""
+    if stream is not None:
+        return _on(stream, mla_up_proj, o_latent, w_uv, out)
     torch = _get_torch()
     _require(o_latent, "o_latent", "bf16")
     if o_latent.dim() < 3 or tuple(o_latent.shape[-2:]) != (H, R):
@@ -286,7 +275,7 @@ def mla_up_proj(o_latent, w_uv, out=None, stream=None):
     _require(out, "out", "bf16", tuple(o_latent.shape[:-1]) + (D,), optional=True)
     _check_cuda(o_latent, w_uv, out)
     if out is None:
-        out = _new(stream, tuple(o_latent.shape[:-1]) + (D,), torch.bfloat16, o_latent.device)
+        out = torch.empty(*o_latent.shape[:-1], D, dtype=torch.bfloat16, device=o_latent.device)
     _check("mla_up_proj", lib().mla_up_proj(_ptr(o_latent), _ptr(w_uv), _ptr(out), n, H, D, R, _stream(stream)))
     return out
 
@@ -304,27 +293,30 @@ def _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens, seq_lens_
     return B, Q
 
 
-def _attend_outputs(q_tilde, o_latent, lse, want_lse, stream=None):
+def _attend_outputs(q_tilde, o_latent, lse, want_lse):
     torch = _get_torch()
     B, Q = q_tilde.shape[0], q_tilde.shape[1]
     if o_latent is None:
-        o_latent = _new(stream, (B, Q, H, R), torch.bfloat16, q_tilde.device)
+        o_latent = torch.empty(B, Q, H, R, dtype=torch.bfloat16, device=q_tilde.device)
     if lse is None and want_lse:
-        lse = _new(stream, (B, Q, H), torch.float32, q_tilde.device)
+        lse = torch.empty(B, Q, H, dtype=torch.float32, device=q_tilde.device)
     return o_latent, lse
 
 
 def mla_attend_dense(q_tilde, cache, seq_lens=None, scale=SCALE, workspace=None, o_latent=None, lse=None,
                      status=None, want_lse=True, stream=None):
     """q_tilde [B, Q, H, R], cache [B, Lmax, R] (bf16), seq_lens [B] int32 or None."""
+    if stream is not None:
+        return _on(stream, mla_attend_dense, q_tilde, cache, seq_lens, scale, workspace, o_latent, lse, status,
+                   want_lse)
     B, Q = _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens)
     _require(cache, "cache", "bf16", (None, None, R))
     if cache.shape[0] < B:
         raise ValueError(f"cache holds {cache.shape[0]} sequences, q_tilde {B}")
     _check_cuda(q_tilde, cache, seq_lens, workspace, o_latent, lse, status)
     Lmax = cache.shape[1]
-    workspace = new_workspace(B, Q, stream) if workspace is None else workspace
-    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse, stream)
+    workspace = new_workspace(B, Q) if workspace is None else workspace
+    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
     _check("mla_attend_dense", lib().mla_attend_dense(
         _ptr(q_tilde), _ptr(cache), _ptr(seq_lens), B, Q, H, R, Lmax, scale, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _ptr(o_latent), _ptr(lse), _ptr(status), _stream(stream)))
@@ -335,12 +327,14 @@ def mla_attend_dense_noalloc(q_tilde, cache, seq_lens=None, scale=SCALE, o_laten
                              want_lse=True, stream=None):
     """mla_attend_dense without a workspace argument: for callers that cannot allocate
     device memory, the scratch is a fixed 32 MiB array inside the library (see mla.h)."""
+    if stream is not None:
+        return _on(stream, mla_attend_dense_noalloc, q_tilde, cache, seq_lens, scale, o_latent, lse, status, want_lse)
     B, Q = _check_attend(q_tilde, None, o_latent, lse, status, seq_lens)
     _require(cache, "cache", "bf16", (None, None, R))
     if cache.shape[0] < B:
         raise ValueError(f"cache holds {cache.shape[0]} sequences, q_tilde {B}")
     _check_cuda(q_tilde, cache, seq_lens, o_latent, lse, status)
-    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse, stream)
+    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
     _check("mla_attend_dense_noalloc", lib().mla_attend_dense_noalloc(
         _ptr(q_tilde), _ptr(cache), _ptr(seq_lens), B, Q, H, R, cache.shape[1], scale, _ptr(o_latent), _ptr(lse),
         _ptr(status), _stream(stream)))
@@ -350,14 +344,17 @@ def mla_attend_dense_noalloc(q_tilde, cache, seq_lens=None, scale=SCALE, o_laten
 def mla_attend_paged(q_tilde, pool, page_table, seq_lens, scale=SCALE, workspace=None, o_latent=None, lse=None,
                      status=None, want_lse=True, stream=None):
     """pool [P, 64, R] bf16, page_table [B, max_pages] int32, seq_lens [B] int32."""
+    if stream is not None:
+        return _on(stream, mla_attend_paged, q_tilde, pool, page_table, seq_lens, scale, workspace, o_latent, lse,
+                   status, want_lse)
     B, Q = _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens, seq_lens_required=True)
     _require(pool, "pool", "bf16", (None, PAGE, R))
     _require(page_table, "page_table", "i32", (None, None))
     if page_table.shape[0] < B:
         raise ValueError(f"page_table has {page_table.shape[0]} rows, q_tilde {B} sequences")
     _check_cuda(q_tilde, pool, page_table, seq_lens, workspace, o_latent, lse, status)
-    workspace = new_workspace(B, Q, stream) if workspace is None else workspace
-    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse, stream)
+    workspace = new_workspace(B, Q) if workspace is None else workspace
+    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
     _check("mla_attend_paged", lib().mla_attend_paged(
         _ptr(q_tilde), _ptr(pool), _ptr(page_table), _ptr(seq_lens), B, Q, H, R, pool.shape[1],
         page_table.shape[1], pool.shape[0], scale, _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -368,14 +365,17 @@ def mla_attend_paged(q_tilde, pool, page_table, seq_lens, scale=SCALE, workspace
 def mla_attend_indexed(q_tilde, cache, indices, seq_lens=None, scale=SCALE, workspace=None, o_latent=None, lse=None,
                        status=None, want_lse=True, stream=None):
     """cache [B, Lmax, R] bf16, indices [B, Q, K] int32."""
+    if stream is not None:
+        return _on(stream, mla_attend_indexed, q_tilde, cache, indices, seq_lens, scale, workspace, o_latent, lse,
+                   status, want_lse)
     B, Q = _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens)
     _require(cache, "cache", "bf16", (None, None, R))
     if cache.shape[0] < B:
         raise ValueError(f"cache holds {cache.shape[0]} sequences, q_tilde {B}")
     _require(indices, "indices", "i32", (B, Q, None))
     _check_cuda(q_tilde, cache, indices, seq_lens, workspace, o_latent, lse, status)
-    workspace = new_workspace(B, Q, stream) if workspace is None else workspace
-    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse, stream)
+    workspace = new_workspace(B, Q) if workspace is None else workspace
+    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
     _check("mla_attend_indexed", lib().mla_attend_indexed(
         _ptr(q_tilde), _ptr(cache), _ptr(indices), _ptr(seq_lens), B, Q, H, R, cache.shape[1], indices.shape[2],
         scale, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(o_latent), _ptr(lse),
@@ -386,16 +386,17 @@ def mla_attend_indexed(q_tilde, cache, indices, seq_lens=None, scale=SCALE, work
 def mla_attend_window_dense(q_tilde, cache, window, sinks=0, seq_lens=None, scale=SCALE, workspace=None, o_latent=None,
                             lse=None, status=None, want_lse=True, stream=None):
     """mla_attend_dense where each query sees its last `window` rows and the first `sinks` ones."""
+    if stream is not None:
+        return _on(stream, mla_attend_window_dense, q_tilde, cache, window, sinks, seq_lens, scale, workspace,
+                   o_latent, lse, status, want_lse)
     _require_int32(window=window, sinks=sinks)
     B, Q = _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens)
     _require(cache, "cache", "bf16", (None, None, R))
     if cache.shape[0] < B:
         raise ValueError(f"cache holds {cache.shape[0]} sequences, q_tilde {B}")
     _check_current(q_tilde, cache, seq_lens, workspace, o_latent, lse, status)
-    with _allocating_on(stream):
-        workspace = new_workspace(B, Q) if workspace is None else workspace
-        o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
-    _read_here(stream, o_latent, lse)
+    workspace = new_workspace(B, Q) if workspace is None else workspace
+    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
     _check("mla_attend_window_dense", lib().mla_attend_window_dense(
         _ptr(q_tilde), _ptr(cache), _ptr(seq_lens), B, Q, H, R, cache.shape[1], scale, window, sinks, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _ptr(o_latent), _ptr(lse), _ptr(status), _stream(stream)))
@@ -405,6 +406,9 @@ def mla_attend_window_dense(q_tilde, cache, window, sinks=0, seq_lens=None, scal
 def mla_attend_window_paged(q_tilde, pool, page_table, seq_lens, window, sinks=0, scale=SCALE, workspace=None,
                             o_latent=None, lse=None, status=None, want_lse=True, stream=None):
     """Paged counterpart of mla_attend_window_dense (pool [P, 64, R], page_table [B, max_pages])."""
+    if stream is not None:
+        return _on(stream, mla_attend_window_paged, q_tilde, pool, page_table, seq_lens, window, sinks, scale,
+                   workspace, o_latent, lse, status, want_lse)
     _require_int32(window=window, sinks=sinks)
     B, Q = _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens, seq_lens_required=True)
     _require(pool, "pool", "bf16", (None, PAGE, R))
@@ -412,10 +416,8 @@ def mla_attend_window_paged(q_tilde, pool, page_table, seq_lens, window, sinks=0
     if page_table.shape[0] < B:
         raise ValueError(f"page_table has {page_table.shape[0]} rows, q_tilde {B} sequences")
     _check_current(q_tilde, pool, page_table, seq_lens, workspace, o_latent, lse, status)
-    with _allocating_on(stream):
-        workspace = new_workspace(B, Q) if workspace is None else workspace
-        o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
-    _read_here(stream, o_latent, lse)
+    workspace = new_workspace(B, Q) if workspace is None else workspace
+    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
     _check("mla_attend_window_paged", lib().mla_attend_window_paged(
         _ptr(q_tilde), _ptr(pool), _ptr(page_table), _ptr(seq_lens), B, Q, H, R, pool.shape[1], page_table.shape[1],
         pool.shape[0], scale, window, sinks, _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -423,15 +425,15 @@ def mla_attend_window_paged(q_tilde, pool, page_table, seq_lens, window, sinks=0
     return o_latent, lse
 
 
-def _fused_outputs(q_tilde, w_uv, out, o_latent, lse, want_lse, stream):
+def _fused_outputs(q_tilde, w_uv, out, o_latent, lse, want_lse):
     torch = _get_torch()
     B, Q = q_tilde.shape[0], q_tilde.shape[1]
     _require(w_uv, "w_uv", "bf16", (H, D, R))
     _require(out, "out", "bf16", (B, Q, H, D), optional=True)
     if out is None:
-        out = _new(stream, (B, Q, H, D), torch.bfloat16, q_tilde.device)
+        out = torch.empty(B, Q, H, D, dtype=torch.bfloat16, device=q_tilde.device)
     if lse is None and want_lse:
-        lse = _new(stream, (B, Q, H), torch.float32, q_tilde.device)
+        lse = torch.empty(B, Q, H, dtype=torch.float32, device=q_tilde.device)
     return out, lse
 
 
@@ -440,13 +442,16 @@ def mla_attend_up_dense(q_tilde, cache, w_uv, seq_lens=None, scale=SCALE, worksp
     """Attention over a contiguous cache with the W_UV up-projection fused into the split-L
     merge: q_tilde [B, Q, H, R], cache [B, Lmax, R], w_uv [H, D, R] -> out [B, Q, H, D]
     (and lse); o_latent [B, Q, H, R] is written too when given."""
+    if stream is not None:
+        return _on(stream, mla_attend_up_dense, q_tilde, cache, w_uv, seq_lens, scale, workspace, out, o_latent, lse,
+                   status, want_lse)
     B, Q = _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens)
     _require(cache, "cache", "bf16", (None, None, R))
     if cache.shape[0] < B:
         raise ValueError(f"cache holds {cache.shape[0]} sequences, q_tilde {B}")
-    out, lse = _fused_outputs(q_tilde, w_uv, out, o_latent, lse, want_lse, stream)
+    out, lse = _fused_outputs(q_tilde, w_uv, out, o_latent, lse, want_lse)
     _check_cuda(q_tilde, cache, w_uv, seq_lens, workspace, out, o_latent, lse, status)
-    workspace = new_workspace(B, Q, stream) if workspace is None else workspace
+    workspace = new_workspace(B, Q) if workspace is None else workspace
     _check("mla_attend_up_dense", lib().mla_attend_up_dense(
         _ptr(q_tilde), _ptr(cache), _ptr(seq_lens), B, Q, H, R, cache.shape[1], scale, _ptr(w_uv), D,
         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out), _ptr(o_latent), _ptr(lse),
@@ -457,14 +462,17 @@ def mla_attend_up_dense(q_tilde, cache, w_uv, seq_lens=None, scale=SCALE, worksp
 def mla_attend_up_paged(q_tilde, pool, page_table, seq_lens, w_uv, scale=SCALE, workspace=None, out=None,
                         o_latent=None, lse=None, status=None, want_lse=True, stream=None):
     """Paged counterpart of mla_attend_up_dense (pool [P, 64, R], page_table [B, max_pages])."""
+    if stream is not None:
+        return _on(stream, mla_attend_up_paged, q_tilde, pool, page_table, seq_lens, w_uv, scale, workspace, out,
+                   o_latent, lse, status, want_lse)
     B, Q = _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens, seq_lens_required=True)
     _require(pool, "pool", "bf16", (None, PAGE, R))
     _require(page_table, "page_table", "i32", (None, None))
     if page_table.shape[0] < B:
         raise ValueError(f"page_table has {page_table.shape[0]} rows, q_tilde {B} sequences")
-    out, lse = _fused_outputs(q_tilde, w_uv, out, o_latent, lse, want_lse, stream)
+    out, lse = _fused_outputs(q_tilde, w_uv, out, o_latent, lse, want_lse)
     _check_cuda(q_tilde, pool, page_table, seq_lens, w_uv, workspace, out, o_latent, lse, status)
-    workspace = new_workspace(B, Q, stream) if workspace is None else workspace
+    workspace = new_workspace(B, Q) if workspace is None else workspace
     _check("mla_attend_up_paged", lib().mla_attend_up_paged(
         _ptr(q_tilde), _ptr(pool), _ptr(page_table), _ptr(seq_lens), B, Q, H, R, pool.shape[1], page_table.shape[1],
         pool.shape[0], scale, _ptr(w_uv), D, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out),
@@ -475,14 +483,17 @@ def mla_attend_up_paged(q_tilde, pool, page_table, seq_lens, w_uv, scale=SCALE, 
 def mla_attend_up_indexed(q_tilde, cache, indices, w_uv, seq_lens=None, scale=SCALE, workspace=None, out=None,
                           o_latent=None, lse=None, status=None, want_lse=True, stream=None):
     """Index-list counterpart of mla_attend_up_dense (indices [B, Q, K] int32)."""
+    if stream is not None:
+        return _on(stream, mla_attend_up_indexed, q_tilde, cache, indices, w_uv, seq_lens, scale, workspace, out,
+                   o_latent, lse, status, want_lse)
     B, Q = _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens)
     _require(cache, "cache", "bf16", (None, None, R))
     if cache.shape[0] < B:
         raise ValueError(f"cache holds {cache.shape[0]} sequences, q_tilde {B}")
     _require(indices, "indices", "i32", (B, Q, None))
-    out, lse = _fused_outputs(q_tilde, w_uv, out, o_latent, lse, want_lse, stream)
+    out, lse = _fused_outputs(q_tilde, w_uv, out, o_latent, lse, want_lse)
     _check_cuda(q_tilde, cache, indices, w_uv, seq_lens, workspace, out, o_latent, lse, status)
-    workspace = new_workspace(B, Q, stream) if workspace is None else workspace
+    workspace = new_workspace(B, Q) if workspace is None else workspace
     _check("mla_attend_up_indexed", lib().mla_attend_up_indexed(
         _ptr(q_tilde), _ptr(cache), _ptr(indices), _ptr(seq_lens), B, Q, H, R, cache.shape[1], indices.shape[2],
         scale, _ptr(w_uv), D, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out),
@@ -492,6 +503,8 @@ def mla_attend_up_indexed(q_tilde, cache, indices, w_uv, seq_lens=None, scale=SC
 
 def mla_expand_kv(c, w_uk, w_uv, k=None, v=None, stream=None):
     """Keys and values of every head from the latents: c [..., R] bf16 -> k, v [..., H, D]."""
+    if stream is not None:
+        return _on(stream, mla_expand_kv, c, w_uk, w_uv, k, v)
     torch = _get_torch()
     _require(c, "c", "bf16")
     if c.dim() < 1 or c.shape[-1] != R:
@@ -503,8 +516,8 @@ def mla_expand_kv(c, w_uk, w_uv, k=None, v=None, stream=None):
     _require(k, "k", "bf16", shape, optional=True)
     _require(v, "v", "bf16", shape, optional=True)
     _check_cuda(c, w_uk, w_uv, k, v)
-    k = _new(stream, shape, torch.bfloat16, c.device) if k is None else k
-    v = _new(stream, shape, torch.bfloat16, c.device) if v is None else v
+    k = torch.empty(shape, dtype=torch.bfloat16, device=c.device) if k is None else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=c.device) if v is None else v
     _check("mla_expand_kv", lib().mla_expand_kv(_ptr(c), _ptr(w_uk), _ptr(w_uv), _ptr(k), _ptr(v), n, H, D, R,
                                                 _stream(stream)))
     return k, v
@@ -512,6 +525,8 @@ def mla_expand_kv(c, w_uk, w_uv, k=None, v=None, stream=None):
 
 def mla_prefill_expanded(q, k, v, scale=SCALE, out=None, lse=None, status=None, want_lse=True, stream=None):
     """Causal self-attention of B sequences of L tokens: q, k, v [B, L, H, D] bf16 -> out (and lse)."""
+    if stream is not None:
+        return _on(stream, mla_prefill_expanded, q, k, v, scale, out, lse, status, want_lse)
     torch = _get_torch()
     _require(q, "q", "bf16", (None, None, H, D))
     B, L = int(q.shape[0]), int(q.shape[1])
@@ -521,9 +536,9 @@ def mla_prefill_expanded(q, k, v, scale=SCALE, out=None, lse=None, status=None, 
     _require(lse, "lse", "f32", (B, L, H), optional=True)
     _require(status, "status", "i32", min_numel=1, optional=True)
     _check_cuda(q, k, v, out, lse, status)
-    out = _new(stream, (B, L, H, D), torch.bfloat16, q.device) if out is None else out
+    out = torch.empty(B, L, H, D, dtype=torch.bfloat16, device=q.device) if out is None else out
     if lse is None and want_lse:
-        lse = _new(stream, (B, L, H), torch.float32, q.device)
+        lse = torch.empty(B, L, H, dtype=torch.float32, device=q.device)
     _check("mla_prefill_expanded", lib().mla_prefill_expanded(
         _ptr(q), _ptr(k), _ptr(v), B, L, H, D, scale, _ptr(out), _ptr(lse), _ptr(status), _stream(stream)))
     return out, lse
@@ -531,6 +546,8 @@ def mla_prefill_expanded(q, k, v, scale=SCALE, out=None, lse=None, status=None, 
 
 def mla_debug_gather(mode, src, req, page_table=None, indices=None, B=None, Q=1, Lmax=0, status=None, stream=None):
     """Rows the attend kernels would address for requests req [n, 3] int32 (b, i, k)."""
+    if stream is not None:
+        return _on(stream, mla_debug_gather, mode, src, req, page_table, indices, B, Q, Lmax, status)
     torch = _get_torch()
     _require(src, "src", "bf16", (None, None, R))
     _require(req, "req", "i32", (None, 3))
@@ -539,7 +556,7 @@ def mla_debug_gather(mode, src, req, page_table=None, indices=None, B=None, Q=1,
     _require(status, "status", "i32", min_numel=1, optional=True)
     _check_cuda(src, req, page_table, indices, status)
     n = req.shape[0]
-    out = _new(stream, (n, R), torch.bfloat16, src.device)
+    out = torch.empty(n, R, dtype=torch.bfloat16, device=src.device)
     max_pages = page_table.shape[1] if page_table is not None else 0
     num_pages = src.shape[0] if mode == MODE_PAGED else 0
     K = indices.shape[2] if indices is not None else 0
@@ -645,6 +662,8 @@ def mla_cache_truncate_packed(pool, page_table, seq_lens, keep, q_len, status=No
 
 def mla_cache_unpack(pool, page_table, start, n, unit=1.0, rows=None, status=None, stream=None):
     """The values of positions start[b] .. start[b] + n - 1 of a 4-bit pool: rows [B, n, R] bf16."""
+    if stream is not None:
+        return _on(stream, mla_cache_unpack, pool, page_table, start, n, unit, rows, status)
     _require_int32(n=n)
     torch = _get_torch()
     _require(start, "start", "i32", (None,))
@@ -652,10 +671,8 @@ def mla_cache_unpack(pool, page_table, start, n, unit=1.0, rows=None, status=Non
     _check_packed(pool, page_table, B, "start", status)
     _require(rows, "rows", "bf16", (B, n, R), optional=True)
     _check_current(pool, page_table, start, rows, status)
-    with _allocating_on(stream):
-        if rows is None:
-            rows = torch.empty(B, n, R, dtype=torch.bfloat16, device=pool.device)
-    _read_here(stream, rows)
+    if rows is None:
+        rows = torch.empty(B, n, R, dtype=torch.bfloat16, device=pool.device)
     _check("mla_cache_unpack", lib().mla_cache_unpack(
         _ptr(pool), _ptr(page_table), _ptr(start), _ptr(rows), B, n, R, PAGE, page_table.shape[1], pool.shape[0],
         unit, _ptr(status), _stream(stream)))
@@ -666,14 +683,15 @@ def mla_attend_packed(q_tilde, pool, page_table, seq_lens, unit=1.0, window=0, s
                       o_latent=None, lse=None, status=None, want_lse=True, stream=None):
     """Attention over a 4-bit pool [P, 64, 288] uint8; with window > 0 each query sees its last
     `window` rows and the first `sinks` ones."""
+    if stream is not None:
+        return _on(stream, mla_attend_packed, q_tilde, pool, page_table, seq_lens, unit, window, sinks, scale,
+                   workspace, o_latent, lse, status, want_lse)
     _require_int32(window=window, sinks=sinks)
     B, Q = _check_attend(q_tilde, workspace, o_latent, lse, status, seq_lens, seq_lens_required=True)
     _check_packed(pool, page_table, B, "q_tilde", status)
     _check_current(q_tilde, pool, page_table, seq_lens, workspace, o_latent, lse, status)
-    with _allocating_on(stream):
-        workspace = new_workspace(B, Q) if workspace is None else workspace
-        o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
-    _read_here(stream, o_latent, lse)
+    workspace = new_workspace(B, Q) if workspace is None else workspace
+    o_latent, lse = _attend_outputs(q_tilde, o_latent, lse, want_lse)
     _check("mla_attend_packed", lib().mla_attend_packed(
         _ptr(q_tilde), _ptr(pool), _ptr(page_table), _ptr(seq_lens), B, Q, H, R, PAGE, page_table.shape[1],
         pool.shape[0], unit, window, sinks, scale, _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -718,14 +736,14 @@ def _check_page_pool(pool, refs, n, workspace):
 
 def mla_pages_reserve(pool, page_table, seq_lens, refs, q_len, workspace=None, status=None, stream=None):
     """Map pages for the next q_len rows of every sequence; shared pages among them become own copies."""
+    if stream is not None:
+        return _on(stream, mla_pages_reserve, pool, page_table, seq_lens, refs, q_len, workspace, status)
     _require_int32(q_len=q_len)
     _check_pages(page_table, refs, status, seq_lens)
     B, max_pages = page_table.shape
     page_bytes, P = _check_page_pool(pool, refs, B, workspace)
     _check_current(pool, page_table, seq_lens, refs, workspace, status)
-    if workspace is None:
-        with _allocating_on(stream):
-            workspace = new_pages_workspace(B, P)
+    workspace = new_pages_workspace(B, P) if workspace is None else workspace
     _check("mla_pages_reserve", lib().mla_pages_reserve(
         _ptr(pool), page_bytes, _ptr(page_table), _ptr(seq_lens), _ptr(refs), B, q_len, max_pages, P,
         _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
@@ -733,6 +751,8 @@ def mla_pages_reserve(pool, page_table, seq_lens, refs, q_len, workspace=None, s
 
 def mla_pages_fork(pool, page_table, seq_lens, refs, parents, children, workspace=None, status=None, stream=None):
     """Sequence children[k] (empty) becomes a copy of sequence parents[k] that shares its full pages."""
+    if stream is not None:
+        return _on(stream, mla_pages_fork, pool, page_table, seq_lens, refs, parents, children, workspace, status)
     _check_pages(page_table, refs, status, seq_lens)
     _require(parents, "parents", "i32", (None,))
     n = parents.shape[0]
@@ -740,9 +760,7 @@ def mla_pages_fork(pool, page_table, seq_lens, refs, parents, children, workspac
     B, max_pages = page_table.shape
     page_bytes, P = _check_page_pool(pool, refs, n, workspace)
     _check_current(pool, page_table, seq_lens, refs, parents, children, workspace, status)
-    if workspace is None:
-        with _allocating_on(stream):
-            workspace = new_pages_workspace(n, P)
+    workspace = new_pages_workspace(n, P) if workspace is None else workspace
     _check("mla_pages_fork", lib().mla_pages_fork(
         _ptr(pool), page_bytes, _ptr(page_table), _ptr(seq_lens), _ptr(refs), _ptr(parents), _ptr(children), n, B,
         max_pages, P, _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
@@ -760,16 +778,16 @@ def mla_pages_release(page_table, seq_lens, refs, status=None, stream=None):
 
 def mla_pages_compact(pool, page_table, refs, n_used=None, workspace=None, status=None, stream=None):
     """Move the used pages to the front of the pool; returns n_used [1] int32, their number."""
+    if stream is not None:
+        return _on(stream, mla_pages_compact, pool, page_table, refs, n_used, workspace, status)
     torch = _get_torch()
     _check_pages(page_table, refs, status, lens_required=False)
     _require(n_used, "n_used", "i32", min_numel=1, optional=True)
     page_bytes, P = _check_page_pool(pool, refs, 1, workspace)
     _check_current(pool, page_table, refs, n_used, workspace, status)
-    with _allocating_on(stream):
-        if n_used is None:
-            n_used = torch.empty(1, dtype=torch.int32, device=pool.device)
-        workspace = new_pages_workspace(1, P) if workspace is None else workspace
-    _read_here(stream, n_used)
+    if n_used is None:
+        n_used = torch.empty(1, dtype=torch.int32, device=pool.device)
+    workspace = new_pages_workspace(1, P) if workspace is None else workspace
     _check("mla_pages_compact", lib().mla_pages_compact(
         _ptr(pool), page_bytes, _ptr(page_table), _ptr(refs), page_table.shape[0], page_table.shape[1], P,
         _ptr(n_used), _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)))
@@ -785,6 +803,8 @@ def mla_debug_wait_timeout(limit_cycles, status, stream=None):
 
 def mla_kpool_keys(cache, pool, seq_lens=None, pooled=None, stream=None):
     """Pooled keys [B, Lmax // pool, R] fp32 of every complete pool of cache [B, Lmax, R]."""
+    if stream is not None:
+        return _on(stream, mla_kpool_keys, cache, pool, seq_lens, pooled)
     torch = _get_torch()
     _require(cache, "cache", "bf16", (None, None, R))
     B, Lmax = cache.shape[0], cache.shape[1]
@@ -794,7 +814,7 @@ def mla_kpool_keys(cache, pool, seq_lens=None, pooled=None, stream=None):
     _require(pooled, "pooled", "f32", (B, Lmax // pool, R), optional=True)
     _check_cuda(cache, seq_lens, pooled)
     if pooled is None:
-        pooled = _new(stream, (B, Lmax // pool, R), torch.float32, cache.device, torch.zeros)
+        pooled = torch.zeros(B, Lmax // pool, R, dtype=torch.float32, device=cache.device)
     _check("mla_kpool_keys", lib().mla_kpool_keys(_ptr(cache), _ptr(seq_lens), B, R, Lmax, pool, _ptr(pooled),
                                                   _stream(stream)))
     return pooled
@@ -802,6 +822,8 @@ def mla_kpool_keys(cache, pool, seq_lens=None, pooled=None, stream=None):
 
 def mla_kpool_select(pooled, w_query, pool, topk, seq_lens=None, with_tail=True, Lmax=None, stream=None):
     """Index lists [B, Q, topk (+ pool - 1)] int32 for w_query [B, Q, R] bf16."""
+    if stream is not None:
+        return _on(stream, mla_kpool_select, pooled, w_query, pool, topk, seq_lens, with_tail, Lmax)
     torch = _get_torch()
     _require(w_query, "w_query", "bf16", (None, None, R))
     B, Q = w_query.shape[0], w_query.shape[1]
@@ -814,7 +836,7 @@ def mla_kpool_select(pooled, w_query, pool, topk, seq_lens=None, with_tail=True,
         raise ValueError(f"pooled holds {pooled.shape[1]} pools per sequence, Lmax {Lmax} needs {Lmax // pool}")
     _check_cuda(pooled, w_query, seq_lens)
     W = topk + (pool - 1 if with_tail else 0)
-    out = _new(stream, (B, Q, W), torch.int32, w_query.device)
+    out = torch.empty(B, Q, W, dtype=torch.int32, device=w_query.device)
     _check("mla_kpool_select", lib().mla_kpool_select(
         _ptr(pooled), _ptr(w_query), _ptr(seq_lens), B, Q, R, Lmax, pool, topk, 1 if with_tail else 0, _ptr(out), W,
         _stream(stream)))
@@ -829,34 +851,35 @@ def mla_decode(q, w_uk, w_uv, cache, seq_lens=None, *, mode=MODE_DENSE, page_tab
     packed (4-bit) cache.
 
     q [B, Q, H, D] bf16 -> out [B, Q, H, D] bf16 (and lse [B, Q, H])."""
+    if stream is not None:
+        return _on(stream, lambda: mla_decode(q, w_uk, w_uv, cache, seq_lens, mode=mode, page_table=page_table,
+                                              indices=indices, scale=scale, workspace=workspace, status=status,
+                                              fused=fused, window=window, sinks=sinks, unit=unit))
     if fused and (window or mode == MODE_PACKED):
         raise ValueError("fused=True has no windowed or packed form")
     if window and mode == MODE_INDEXED:
         raise ValueError("index lists take no window")
     if window or mode == MODE_PACKED:  # as their attention refuses it, before anything is launched
-        _check_current(q, w_uk, w_uv, cache, seq_lens, page_table, workspace, status)
-    qt = mla_absorb_q(q, w_uk, stream=stream)
+        _check_current(q, w_uk)
+    qt = mla_absorb_q(q, w_uk)
     if fused:
         if mode == MODE_DENSE:
-            return mla_attend_up_dense(qt, cache, w_uv, seq_lens, scale, workspace, status=status, stream=stream)
+            return mla_attend_up_dense(qt, cache, w_uv, seq_lens, scale, workspace, status=status)
         if mode == MODE_PAGED:
-            return mla_attend_up_paged(qt, cache, page_table, seq_lens, w_uv, scale, workspace, status=status,
-                                       stream=stream)
-        return mla_attend_up_indexed(qt, cache, indices, w_uv, seq_lens, scale, workspace, status=status,
-                                     stream=stream)
+            return mla_attend_up_paged(qt, cache, page_table, seq_lens, w_uv, scale, workspace, status=status)
+        return mla_attend_up_indexed(qt, cache, indices, w_uv, seq_lens, scale, workspace, status=status)
     if mode == MODE_PACKED:
         o, lse = mla_attend_packed(qt, cache, page_table, seq_lens, unit, window, sinks, scale, workspace,
-                                   status=status, stream=stream)
+                                   status=status)
     elif mode == MODE_DENSE and window:
-        o, lse = mla_attend_window_dense(qt, cache, window, sinks, seq_lens, scale, workspace, status=status,
-                                         stream=stream)
+        o, lse = mla_attend_window_dense(qt, cache, window, sinks, seq_lens, scale, workspace, status=status)
     elif mode == MODE_PAGED and window:
         o, lse = mla_attend_window_paged(qt, cache, page_table, seq_lens, window, sinks, scale, workspace,
-                                         status=status, stream=stream)
+                                         status=status)
     elif mode == MODE_DENSE:
-        o, lse = mla_attend_dense(qt, cache, seq_lens, scale, workspace, status=status, stream=stream)
+        o, lse = mla_attend_dense(qt, cache, seq_lens, scale, workspace, status=status)
     elif mode == MODE_PAGED:
-        o, lse = mla_attend_paged(qt, cache, page_table, seq_lens, scale, workspace, status=status, stream=stream)
+        o, lse = mla_attend_paged(qt, cache, page_table, seq_lens, scale, workspace, status=status)
     else:
-        o, lse = mla_attend_indexed(qt, cache, indices, seq_lens, scale, workspace, status=status, stream=stream)
-    return mla_up_proj(o, w_uv, stream=stream), lse
+        o, lse = mla_attend_indexed(qt, cache, indices, seq_lens, scale, workspace, status=status)
+    return mla_up_proj(o, w_uv), lse

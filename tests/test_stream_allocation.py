@@ -3,6 +3,7 @@ still be written by kernels pending there, and is handed on there when the call 
 tells the allocator that its results are read on the current stream.  Without a GPU: the library is
 a stand-in that launches nothing, and the allocations are recorded."""
 import contextlib
+import types
 
 import pytest
 import torch
@@ -28,8 +29,7 @@ class Record:
         monkeypatch.setattr(m, "_check_cuda", lambda *t: 0)
         monkeypatch.setattr(m, "_check_current", lambda *t: None)
         monkeypatch.setattr(m, "_stream", lambda s: 0)
-        monkeypatch.setattr(m, "_allocating_on", self.allocating_on)
-        monkeypatch.setattr(m, "_read_here", lambda s, *t: self.read.extend(id(x) for x in t if x is not None))
+        monkeypatch.setattr(m, "_on", self.on)
 
     def allocator(self, make):
         def wrapped(*shape, **kw):
@@ -39,11 +39,13 @@ class Record:
             return t
         return wrapped
 
-    @contextlib.contextmanager
-    def allocating_on(self, stream):
-        before, self.inside = self.inside, self.inside or stream is S
-        yield
-        self.inside = before
+    def on(self, stream, call, *args):
+        assert stream is S and not self.inside
+        self.inside = True
+        out = call(*args)
+        self.inside = False
+        self.read += [id(t) for t in (out if isinstance(out, tuple) else (out,))]
+        return out
 
 
 def bf(*shape):
@@ -101,12 +103,38 @@ def test_allocations_are_the_streams(monkeypatch, name):
         assert t is None or id(t) in r.read
 
 
-def test_a_stream_of_another_device_is_refused(monkeypatch):
-    class Stream:
-        device_index = 1
+def _streams(monkeypatch):
+    """torch.cuda's current stream, without a device: "caller" until a context changes it."""
+    now = ["caller"]
+
+    @contextlib.contextmanager
+    def use(stream):
+        before, now[0] = now[0], stream
+        yield
+        now[0] = before
+
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "stream", use)
+
+
+def test_on_a_stream(monkeypatch):
+    """The call runs with the stream as the current one, and its results are recorded for the caller's."""
+    _streams(monkeypatch)
+    stream, recorded = types.SimpleNamespace(device_index=0), []
+    results = tuple(types.SimpleNamespace(record_stream=lambda s, k=k: recorded.append((k, s))) for k in range(2))
+    for out, n in ((results, 2), (results[0], 1), ((results[0], None), 1), (None, 0)):
+        recorded.clear()
+        assert m._on(stream, lambda a, b: (torch.cuda.current_stream(), a, b) == (stream, 1, 2) and out, 1, 2) == out
+        assert recorded == [(k, "caller") for k in range(n)]
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    _streams(monkeypatch)
+    called = []
     with pytest.raises(ValueError, match="the stream is on cuda:1, the current device is cuda:0"):
-        m._allocating_on(Stream())
+        m._on(types.SimpleNamespace(device_index=1), called.append, 1)
+    assert not called
 
 
 @pytest.mark.parametrize("name", ["decode_window", "decode_window_paged", "decode_packed"])
