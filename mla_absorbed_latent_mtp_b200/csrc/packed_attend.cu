@@ -12,9 +12,12 @@
 // codes cannot be an operand as they are, since each row has its own scales.  So the cache
 // operand is unpacked into TENSOR memory, twice, by register, and shared memory holds only the
 // packed rows, q~ and P.  Measured: 5,300 cycles a tile, 2.6 times the MMAs' own; the rest is the
-// unpacking, the softmax and the hand-overs between them (3,070 instructions a tile and scheduler).
-// With the merge 32 x 8,192 rows take 67 us, 16 sequences of 1.05 M rows in all 193 us (217 in a
-// long run), 16 x 6 queries with a window of 8,191 rows and 64 sinks 145 to 148 us (152).
+// unpacking, the softmax and the hand-overs between them (3,070 instructions a tile and scheduler),
+// the spills of the roles that 96 registers are too few for among them (524 bytes of stores and 500
+// of loads in the kernel; 1.15 of 30.0 million instructions executed for 32 x 8,192 rows).
+// With the merge 32 x 8,192 rows take 67 us (bf16 rows, attend.cu: 65), 16 sequences of 1.05 M rows
+// in all 193 us at 1,965 MHz (216 at the 1,755 MHz that the power cap leaves in a long run), 16 x 6
+// queries with a window of 8,191 rows and 64 sinks 145 us (150 at 1,890 MHz).
 //   S^T[rows, heads]    = C (A: 128 rows on the lanes, 64 latents a chunk) * Q~^T (smem)
 //   O^T[latent, heads] += C^T (A: 128 latents on the lanes, 16 rows a chunk, x 4) * P^T (smem)
 // Both unpackings read the same packed words.  For C a thread owns a row.  For C^T a thread
@@ -25,9 +28,10 @@
 //
 // Operands are fp16: code * scale is exact there.  q~ (bf16) is converted once per segment with
 // a power of two per head that puts the head's largest value in [2^14, 2^15): exact unless a
-// value is 2^-31 of the largest or less.  P is p * 2^7 in fp16 (p <= 2^8 under the lazy
-// rescale, so at most 2^15; values below 2^-24 of the row's maximum round to nothing), the row
-// sums stay in fp32 of the unrounded p.
+// value is 2^-31 of the largest or less.  P is p * 2^7 in fp16, p = 2^(score - running max) <= 2^8
+// under the lazy rescale, so at most 2^15.  From p = 2^-21 down it is rounded by at most 2^-32 (fp16's
+// subnormal range) instead of 2^-11 of itself, and below 2^-32 to zero, while the head's largest p is
+// at least 1.  The row sums stay in fp32 of the unrounded p.
 //
 // Per CTA 19 warps (five on a scheduler: 96 registers a thread): 0 TMA loads, 1 score MMAs, 2 value
 // MMAs, 3-10 softmax (two groups of four warps, 32 heads each; they also convert q~ and write
@@ -647,7 +651,8 @@ __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint
     // The last segment's scores are done: this one's q~ takes the place of that one's before its
     // O^T is stored, so that the first scores are computed meanwhile (256 x 500 rows: 80.0 us with
     // the store first, 74.9 so; 32 x 8,192: 69.7, 69.2; against it 16 ragged sequences, 214 and 217,
-    // and 16 x 6 queries, window 8,191 + 64, 149 and 152: the loop over tiles is compiled a little worse).
+    // and 16 x 6 queries, window 8,191 + 64, 149 and 152: the code has
+    // 524 bytes of spill stores instead of 460).
     if (more) convert_query(p, sh, sg.b, iq, w, lane);
     if (slot >= 0) {
       wait(bar, kBarOFull, segs & 1);
