@@ -651,8 +651,8 @@ __device__ void softmax_role(const AttendPackedParams &p, const Shared &sh, uint
     // The last segment's scores are done: this one's q~ takes the place of that one's before its
     // O^T is stored, so that the first scores are computed meanwhile (256 x 500 rows: 80.0 us with
     // the store first, 74.9 so; 32 x 8,192: 69.7, 69.2; against it 16 ragged sequences, 214 and 217,
-    // and 16 x 6 queries, window 8,191 + 64, 149 and 152: the code has
-    // 524 bytes of spill stores instead of 460).
+    // and 16 x 6 queries, window 8,191 + 64, 149 and 152: the code has 524 bytes of spill stores
+    // instead of 460).
     if (more) convert_query(p, sh, sg.b, iq, w, lane);
     if (slot >= 0) {
       wait(bar, kBarOFull, segs & 1);

@@ -14,8 +14,8 @@
 //  - the list's ranges allow for what beginning a sequence costs, and the merge has a form for few
 //    sequences with many partials (lists.cuh);
 //  - l sums the unrounded weights, so lse is exact to fp32.  The value product takes them rounded to
-//    bf16: against 64 bits o is off by 0.0018 to 0.0021 of its norm (windows of 2 to 1,024 rows), where
-//    rounding the result alone costs 0.0017.
+//    bf16: against 64 bits o is off by 0.0018 to 0.0022 of its norm (windows of two rows or more),
+//    where rounding the result alone costs 0.0017.
 //
 // What bounds it: as attend.cu, the recycling of ring slots, 3,000 cycles a tile (0.87 of the
 // measured copy peak for distinct rows); around that, for windows of some thousand rows, 20 us of
